@@ -257,9 +257,10 @@ def _run_own(s):
 
 def _plain_table(s):
     need = (s.lens.clamp(min=0).long() + (s.page - 1)) // s.page
+    need = torch.where(need <= s.max_pages, need, 0)
     end = torch.cumsum(need, 0)
     first = s.first.long()
-    fits = (need <= s.max_pages) & (first + end <= s.pool.numel())
+    fits = first + end <= s.pool.numel()
     held = torch.where(fits, need, 0)
     at = torch.arange(s.max_pages, device=need.device)
     src = (first + (end - need)[:, None] + at).clamp(max=s.pool.numel() - 1)
