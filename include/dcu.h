@@ -54,6 +54,9 @@ extern "C" {
 #define DCU_ST_BAD_KEY   1  /* a key position outside [0, N) was ignored */
 #define DCU_ST_BAD_TOKEN 2  /* a token id outside [0, vocab) was clamped   */
 #define DCU_ST_TIMEOUT   4  /* a bounded device wait gave up                */
+#define DCU_ST_BAD_PAGE  8  /* a page id outside the pool, or a length or position past its table row: left out */
+#define DCU_ST_NO_PAGE  16  /* a request got no pages: the pool or its table row is too short */
+#define DCU_ST_BAD_ROW  32  /* more rows than max_rows, rows out of order, or a position past the RoPE table */
 
 /* ---- dtypes, rules, window modes ---- */
 #define DCU_F32   0
@@ -334,6 +337,105 @@ int dcu_linear(const void *X, const void *W, int32_t M, int32_t K, int32_t Nout,
 int dcu_lm_confidence_noalloc(const void *h_rows, const float *final_norm, const void *lm_head, int32_t m,
                               int32_t D, int32_t V, int32_t dtype, float rms_eps, float *conf, int32_t *argmax,
                               dcu_stream_t stream);
+
+/* ---- paged K/V caches (stateless) ----
+ *
+ * Sequences of different lengths share one pool of pages per layer.  A page
+ * holds page_size consecutive key slots of one sequence for every kv head; row
+ * b of a block table lists the pages of sequence b in order, -1 past the last.
+ * Slot page * page_size + offset is the cache place of position p of sequence
+ * b, with page = table[b][p / page_size] and offset = p % page_size.  The calls
+ * below are the stages of a step over such a cache: dcu_page_table once per
+ * batch, dcu_slot_map once per set of rows (idx and count of
+ * dcu_select_tokens, or ranges), then per layer dcu_linear (QKV),
+ * dcu_paged_write, dcu_paged_attention, dcu_linear (O).  The rows of sequence b
+ * are the packed rows [row_start[b], row_start[b + 1]), as in DCU_T_ATTN.
+ *
+ * The counts and lengths stay on the device, so a captured call replays with
+ * whatever they hold then; max_rows (host) bounds the packed rows.  Rows at and
+ * after row_start[B] are neither read nor written.  status (dev int32 or NULL)
+ * gets the DCU_ST_* bits above ORed in; whatever the device arrays hold, no
+ * access leaves the arrays as sized by the host arguments. */
+
+/* One layer's pages.  Element (page, offset, head, d) of K is at
+ * k + page * page_stride + offset * slot_stride + head * head_stride + d
+ * (strides in elements, the same for V), so [n_pages][page_size][n_kv_heads][head_dim]
+ * and [n_pages][n_kv_heads][page_size][head_dim] are both described.  k, v 16-byte
+ * aligned, every stride >= 0 and a multiple of 16 bytes; head_dim % 16 == 0 and <= 256;
+ * n_pages * page_size < 2^31; dtype DCU_F32 or DCU_BF16. */
+typedef struct {
+  void *k, *v;
+  int64_t page_stride, slot_stride, head_stride;
+  int32_t n_pages, page_size, n_kv_heads, head_dim, dtype;
+} dcu_pages;
+
+/* Block table of B requests from their lengths.  Request b needs
+ * ceil(lens[b] / page_size) pages (a length below 1: none) and gets them from
+ * pool[*first ...] in request order: pool dev int32 [n_pool] lists free page ids
+ * (NULL: page i is entry i), first dev int32 (NULL: 0).  A request that needs more
+ * than max_pages gets none and takes nothing from the pool; so does every request
+ * from the first one on that the pool cannot serve whole (DCU_ST_NO_PAGE).  A
+ * pool entry outside [0, n_pages) becomes -1 (DCU_ST_BAD_PAGE).
+ * table: dev int32 [B][max_pages], every entry written; held: dev int32 [B], the
+ * pages each request got; next: dev int32, *first + the pages given out -- the
+ * `first` of the next call on the same pool.  B <= 65536.  `next` may not alias
+ * `first`. */
+int dcu_page_table(const int32_t *lens, int32_t B, int32_t page_size, int32_t max_pages, int32_t n_pages,
+                   const int32_t *pool, int32_t n_pool, const int32_t *first, int32_t *table, int32_t *held,
+                   int32_t *next, int32_t *status, dcu_stream_t stream);
+
+/* Packed rows and their cache slots.  Sequence b has count[b] rows (below 0:
+ * none), at positions pos[b][0 .. count[b]) (pos: dev int32 [B][pos_stride],
+ * strictly ascending, e.g. idx of dcu_select_tokens), or, with pos NULL, at
+ * first[b], first[b] + 1, ... (first: dev int32 [B], NULL: from 0).  Outputs:
+ * row_start dev int32 [B + 1] (prefix sums of count, at most max_rows);
+ * row_pos, slot dev int32 [max_rows].  A position that no page of the sequence
+ * covers gets slot -1 (DCU_ST_BAD_PAGE).  DCU_ST_BAD_ROW: rows past max_rows or
+ * a count above pos_stride (dropped), positions not strictly ascending (kept: if
+ * one repeats, its two rows share a slot).  B <= 65536. */
+int dcu_slot_map(const int32_t *table, int32_t B, int32_t max_pages, int32_t page_size, int32_t n_pages,
+                 const int32_t *count, const int32_t *pos, int32_t pos_stride, const int32_t *first,
+                 int32_t max_rows, int32_t *row_start, int32_t *row_pos, int32_t *slot, int32_t *status,
+                 dcu_stream_t stream);
+
+/* cos / sin table of rotate-half RoPE: tab dev float [max_pos][head_dim / 2][2],
+ * (cos, sin) of pos * theta^(-2j / head_dim), angles in fp64, rounded once (the
+ * table a context uses).  theta > 0. */
+int dcu_rope_table(float *tab, int32_t max_pos, int32_t head_dim, float theta, dcu_stream_t stream);
+
+/* RoPE and the paged K/V write of packed rows: the QKV epilogue of a layer.
+ * qkv: dev float [max_rows][(n_heads + 2 n_kv_heads) * head_dim] (q heads, k
+ * heads, v heads; the output of dcu_linear over stacked wq, wk, wv); n_rows: dev
+ * int32, the rows in use (row_start + B; NULL: max_rows).  q (dev [max_rows][n_heads][head_dim]
+ * in the pages' dtype) gets the rotated queries; K (rotated) and V go to the
+ * row's slot.  rope: the table of dcu_rope_table, NULL for no rotation.  A slot
+ * outside [0, n_pages * page_size) is not written (a slot of -1 silently).  A
+ * row_pos outside [0, max_pos) gives a zero query and no K/V write
+ * (DCU_ST_BAD_ROW; not looked at without rope).  Strides must be positive where
+ * their dimension is above 1, and no two slots may overlap.  Two rows with the same slot
+ * leave a mixture of both there. */
+int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, const int32_t *row_pos,
+                    const int32_t *slot, const float *rope, int32_t max_pos, int32_t n_heads,
+                    const dcu_pages *pages, void *q, int32_t *status, dcu_stream_t stream);
+
+/* Attention of packed query rows over all cached keys of their sequence
+ * (bidirectional): out[r][h] = sum_j softmax_j(scale q[r][h] . K_j) V_j over the
+ * keys j < kv_len[b] of kv head h / (n_heads / n_kv_heads).  One row a sequence
+ * is the single-token form.  q, out: dev [max_rows][n_heads][head_dim] in the
+ * pages' dtype; row_start: dev int32 [B + 1], non-decreasing; kv_len: dev int32
+ * [B]; table: dev int32 [B][max_pages]; out may not overlap q.  Slots at and past kv_len are never
+ * used, whatever they hold; keys on a page outside [0, n_pages) or past the
+ * table row are left out (DCU_ST_BAD_PAGE); a row with no key gives zeros.
+ * The keys are split over the SMs and joined in a fixed order: equal inputs
+ * give equal bits.  workspace: dev, 16-byte aligned, at least
+ * dcu_paged_attention_workspace bytes, any content; calls that may overlap (on
+ * other streams, or in graphs replayed together) need one each.  B <= 65536. */
+int dcu_paged_attention(const void *q, int32_t max_rows, const int32_t *row_start, int32_t B, const int32_t *kv_len,
+                        const int32_t *table, int32_t max_pages, int32_t n_heads, const dcu_pages *pages, float scale,
+                        void *out, void *workspace, int64_t workspace_bytes, int32_t *status, dcu_stream_t stream);
+/* Workspace bytes of dcu_paged_attention on the current device: they depend on
+ * the pages' head_dim and dtype alone. */
+int dcu_paged_attention_workspace(const dcu_pages *pages, int64_t *bytes);
 
 /* ---- introspection (tests, teacher forcing) ---- */
 

@@ -1,0 +1,112 @@
+"""Refusals of the paged K/V cache entry points: checked on the host, no GPU needed."""
+import ctypes
+
+import pytest
+import torch
+
+from dynamic_layer_wise_b200 import build, dcu
+
+P = 4096  # a 16-byte aligned address that is never read
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build_all()
+    return dcu.lib()
+
+
+def _pages(**kw):
+    base = dict(k=P, v=P, page_stride=16 * 4 * 64, slot_stride=4 * 64, head_stride=64, n_pages=8, page_size=16,
+                n_kv_heads=4, head_dim=64, dtype=dcu.DCU_BF16)
+    base.update(kw)
+    return ctypes.byref(dcu.dcu_pages(**base))
+
+
+BAD_PAGES = [dict(k=None), dict(v=None), dict(dtype=5), dict(n_pages=0), dict(page_size=0), dict(n_kv_heads=0),
+             dict(head_dim=24), dict(head_dim=272), dict(head_dim=0), dict(k=P + 8), dict(v=P + 2),
+             dict(page_stride=-64), dict(slot_stride=260), dict(head_stride=68), dict(n_pages=1 << 28),
+             dict(dtype=dcu.DCU_F32, head_stride=66)]
+
+TABLE = dict(lens=P, B=2, page_size=16, max_pages=4, n_pages=8, pool=P, n_pool=8, first=None, table=P, held=P,
+             next=P + 64, status=None, stream=None)
+MAP = dict(table=P, B=2, max_pages=4, page_size=16, n_pages=8, count=P, pos=None, pos_stride=0, first=None,
+           max_rows=4, row_start=P, row_pos=P, slot=P, status=None, stream=None)
+WRITE = dict(qkv=P, max_rows=4, n_rows=P, row_pos=P, slot=P, rope=P, max_pos=64, n_heads=8, pages={}, q=P,
+             status=None, stream=None)
+ATTN = dict(q=P, max_rows=4, row_start=P, B=2, kv_len=P, table=P, max_pages=4, n_heads=8, pages={}, scale=0.125,
+            out=2 * P, ws=P, ws_bytes=1 << 40, status=None, stream=None)
+
+
+def _call(fn, base, **kw):
+    a = dict(base, **kw)
+    if "pages" in a and isinstance(a["pages"], dict):
+        a["pages"] = _pages(**a["pages"])
+    return fn(*a.values())
+
+
+@pytest.mark.parametrize("bad", [dict(lens=None), dict(B=0), dict(B=65537), dict(page_size=0), dict(max_pages=0),
+                                 dict(n_pages=0), dict(n_pages=1 << 30), dict(n_pool=-1), dict(pool=None, n_pool=3),
+                                 dict(table=None), dict(held=None), dict(next=None), dict(first=P + 64)])
+def test_page_table_refusals(L, bad):
+    assert _call(L.dcu_page_table, TABLE, **bad) == dcu.DCU_EINVAL
+    assert b"dcu_page_table" in L.dcu_last_error(None)
+
+
+@pytest.mark.parametrize("bad", [dict(table=None), dict(B=0), dict(B=65537), dict(max_pages=0), dict(page_size=-1),
+                                 dict(n_pages=0), dict(count=None), dict(pos=P), dict(pos=P, pos_stride=4, first=P),
+                                 dict(max_rows=-1), dict(row_start=None), dict(row_pos=None), dict(slot=None)])
+def test_slot_map_refusals(L, bad):
+    assert _call(L.dcu_slot_map, MAP, **bad) == dcu.DCU_EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(qkv=None), dict(max_rows=-1), dict(row_pos=None), dict(slot=None),
+                                 dict(max_pos=0), dict(n_heads=0), dict(q=None), dict(qkv=P + 4), dict(rope=P + 8),
+                                 dict(q=P + 2), dict(pages=dict(slot_stride=0)), dict(pages=dict(page_stride=0)),
+                                 dict(pages=dict(head_stride=0))])
+def test_paged_write_refusals(L, bad):
+    assert _call(L.dcu_paged_write, WRITE, **bad) == dcu.DCU_EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(q=None), dict(max_rows=-1), dict(row_start=None), dict(B=0), dict(B=65537),
+                                 dict(kv_len=None), dict(table=None), dict(max_pages=0), dict(n_heads=0),
+                                 dict(n_heads=6), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38),
+                                 dict(out=None), dict(out=P), dict(q=P + 8), dict(out=P + 4), dict(ws=None),
+                                 dict(ws=P + 8), dict(ws_bytes=0)])
+def test_paged_attention_refusals(L, bad):
+    assert _call(L.dcu_paged_attention, ATTN, **bad) == dcu.DCU_EINVAL
+
+
+@pytest.mark.parametrize("bad", BAD_PAGES)
+def test_page_geometry_refusals(L, bad):
+    n = ctypes.c_int64(0)
+    assert L.dcu_paged_attention_workspace(_pages(**bad), ctypes.byref(n)) == dcu.DCU_EINVAL
+    assert _call(L.dcu_paged_write, WRITE, pages=bad) == dcu.DCU_EINVAL
+    assert _call(L.dcu_paged_attention, ATTN, pages=bad) == dcu.DCU_EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(tab=None), dict(max_pos=0), dict(head_dim=7), dict(theta=0.0),
+                                 dict(theta=float("inf")), dict(theta=float("nan"))])
+def test_rope_table_refusals(L, bad):
+    assert _call(L.dcu_rope_table, dict(tab=P, max_pos=8, head_dim=64, theta=1e4, stream=None), **bad) == dcu.DCU_EINVAL
+
+
+def test_zero_rows_are_no_work(L):
+    assert _call(L.dcu_paged_write, WRITE, max_rows=0, qkv=None, q=None) == dcu.DCU_OK
+    assert _call(L.dcu_paged_attention, ATTN, max_rows=0, q=None, out=None) == dcu.DCU_OK
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_types(L):
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        dcu.dcu_page_table(i, 16, 4, 8)
+    with pytest.raises(TypeError):
+        dcu.dcu_page_table([1, 2], 16, 4, 8)
+    with pytest.raises(ValueError):
+        dcu.dcu_slot_map(i[None], i, 16, 8, 4)
+    k = torch.zeros(2, 16, 4, 64)
+    with pytest.raises(ValueError):
+        dcu.dcu_paged_attention(torch.zeros(3, 8, 64), i, i, i[None], k, k)
+    with pytest.raises(ValueError):
+        dcu.dcu_paged_write(torch.zeros(3, 1024), i, i, i, None, k, k, 8)
+    with pytest.raises(ValueError):
+        dcu.dcu_rope_table(0, 64, device="cuda:0")
