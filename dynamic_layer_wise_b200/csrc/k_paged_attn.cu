@@ -1,78 +1,730 @@
-// Attention of packed query rows over the paged K/V cache of their sequence.
+// Attention of packed query rows over the paged K/V cache of their sequence:
+// out[r][h] = sum_j w_j V_j, w = softmax_j(scale q . K_j) over the keys j of
+// the row's sequence, read through its block table.
+//
+// Work.  A query is a (row, query head) pair; an item is (sequence, kv head,
+// tile of at most R queries), so a tile reads its keys once for the whole GQA
+// group of its rows.  The keys of an item are cut into blocks of KB.  All
+// blocks of all items, in item order, form one line of units that is cut into
+// equal ranges, one per CTA (one CTA per SM): every SM reads the same number of
+// keys whatever the lengths are, a long sequence is split over many SMs and
+// short ones share an SM.  Lengths and rows are only on the device, so each CTA
+// derives the cut itself from the prefix sum of the sequences' unit counts.
+//
+// Inside a CTA the units go round-robin to its warps.  Each warp streams its
+// own blocks through a private ring of shared memory with 16-byte cp.async
+// (zero-filled past the length and for bad pages, so nothing outside the
+// sequence is ever read into a product) and keeps its own running maximum, sum
+// and O = P V, all fp32; nothing but the end of an item synchronises the warps.
+// The ring runs across item ends, so loads keep flowing while a finished item
+// is merged.  Where a CTA's range cuts an item, its share (O, max, sum) goes to
+// the workspace and k_paged_merge joins the shares in range order.
+//
+// bf16 blocks run on mma.sync m16n8k16 with the operands swapped (S^T = K Q^T,
+// O^T += V^T P^T): the 16-wide M holds keys or head dims, the 8-wide N holds
+// queries, so a single token with 7 or 8 heads in a group fills the tile.  P is
+// split into a high and a low bf16 part, two products instead of one: the
+// weights keep 16 bits at a cost that the memory-bound loop hides.  float32
+// blocks run on the CUDA cores in fp32.
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.h"
 
 namespace dcu {
 namespace {
 
-// One warp per (row, head): out = sum_j p_j V_j / sum_j p_j with a running max,
-// a key at a time, the head dim spread over the lanes.
-template <class T>
-__global__ void __launch_bounds__(128) k_paged_attn_rowhead(const PagedAttnArgs a) {
-  pdl_enter();
-  const dcu_pages &pg = a.pages;
-  const int lane = threadIdx.x & 31;
-  const int hd = pg.head_dim, G = a.n_heads / pg.n_kv_heads;
-  const int rows = min(max(a.row_start[a.B], 0), a.max_rows);
-  const long long items = (long long)rows * a.n_heads;
-  const T *Q = static_cast<const T *>(a.q), *K = static_cast<const T *>(pg.k), *V = static_cast<const T *>(pg.v);
-  for (long long it = blockIdx.x * 4ll + (threadIdx.x >> 5); it < items; it += gridDim.x * 4ll) {
-    const int r = (int)(it / a.n_heads), h = (int)(it - (long long)r * a.n_heads);
-    int lo = 0, hi = a.B - 1;  // the first sequence whose end is above r
-    while (lo < hi) {
-      const int m = (lo + hi) >> 1;
-      if (a.row_start[m + 1] > r) hi = m;
-      else lo = m + 1;
-    }
-    const int n = max(a.kv_len[lo], 0);
-    float q[8], o[8], m_run = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = lane + 32 * e;
-      q[e] = d < hd ? to_f(Q[((size_t)r * a.n_heads + h) * hd + d]) : 0.f;
-      o[e] = 0.f;
-    }
-    for (int key = 0; key < n; ++key) {
-      const int pi = key / pg.page_size;
-      const int page = pi < a.max_pages ? a.table[(size_t)lo * a.max_pages + pi] : -1;
-      if (page < 0 || page >= pg.n_pages) {
-        if (lane == 0 && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
-        if (pi >= a.max_pages) break;
-        continue;
-      }
-      const int64_t at = (int64_t)page * pg.page_stride + (int64_t)(key - pi * pg.page_size) * pg.slot_stride +
-                         (int64_t)(h / G) * pg.head_stride;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < hd) s = fmaf(q[e], to_f(K[at + lane + 32 * e]), s);
-      s = warp_sum(s) * a.scale_log2;
-      const float m_new = fmaxf(m_run, s);
-      const float f = m_run == -INFINITY ? 0.f : exp2f(m_run - m_new), p = exp2f(s - m_new);
-      m_run = m_new;
-      l = l * f + p;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (lane + 32 * e < hd) o[e] = fmaf(p, to_f(V[at + lane + 32 * e]), o[e] * f);
-    }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < hd)
-        static_cast<T *>(a.out)[((size_t)r * a.n_heads + h) * hd + lane + 32 * e] = from_f<T>(o[e] * inv);
+constexpr int kMaxRanges = 148;  // most CTAs (work ranges) of a launch
+
+// One kernel variant: head dims up to DP (shorter ones zero-padded in shared memory).
+template <int DP, bool F32>
+struct Cfg {
+  static constexpr int kKB = F32 ? 8 : 16;                       // keys of a block
+  static constexpr int kW = DP == 256 ? 4 : 8;                   // warps
+  static constexpr int kNT = F32 ? 1 : (DP == 256 ? 2 : 4);      // groups of 8 queries in a tile
+  static constexpr int kR = 8 * kNT;                             // queries of a tile
+  static constexpr int kEs = F32 ? 4 : 2;                        // element size
+  static constexpr int kRow = DP * kEs;                          // bytes of a key row
+  static constexpr int kStage = 2 * kKB * kRow;                  // K and V of a block
+  static constexpr int kNst = DP == 64 ? 5 : 3;                  // ring stages of a warp
+  static constexpr int kQPitch = kRow + 16;                      // padded query row
+  static constexpr int kRing = kW * kNst * kStage;
+  static constexpr int kQ = kR * kQPitch;
+  static constexpr int kRed = (kW / 2) * DP * 8 * 4;             // merge buffer: half the warps, 8 queries
+  static constexpr int kP = F32 ? kW * 64 * 4 : 0;               // float32: P of a block, per warp
+  static constexpr int kSmem = kRing + kQ + kRed + kP + 16;
+  static constexpr int kThreads = 32 * kW;
+  static constexpr int kND = F32 ? (DP > 128 ? DP / 128 : 1) : 0;  // float32: 4-dim chunks of O per lane and query
+  static constexpr int kAcc = F32 ? 8 * kND : DP / 16;           // float4s of O per lane and query group
+};
+
+// A share of an item that a range boundary cuts: what the merge needs.
+struct Share {
+  int32_t last;   // last range that holds a share of the item begun in this range; -1: none is cut here
+  int32_t row0;   // first packed row of the sequence
+  int32_t q0;     // first query (pair index in the sequence and kv head) of the tile
+  int32_t nq;     // queries of the tile
+  int32_t kvh;
+  int32_t slot;   // the share of this range: 0 its first segment, 1 its last one
+};
+
+__device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cpa16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cpa_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cpa_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// transpose of an 8 x 8 tile of 16-bit values held one row pair per lane
+__device__ __forceinline__ uint32_t movm(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// 16-byte chunk c of key row r: bits of r spread the rows that are read
+// together over the banks (bf16: the 8 rows of an ldmatrix; float32: the two
+// key rows of a quarter warp).
+template <bool F32>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return F32 ? (uint32_t)(c ^ (((r & 1) << 2) | ((r >> 1) & 3))) : (uint32_t)(c ^ (r & 7));
+}
+
+// The items of sequence b.
+struct Seq {
+  int row0, nq, tiles, tq, nk, nblk;  // first row, queries per kv head, tiles, queries per tile, keys, blocks per item
+  __device__ __forceinline__ long long units(int KV) const { return (long long)KV * tiles * nblk; }
+};
+template <int R, int KB>
+__device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
+  Seq s;
+  const int lo = min(max(a.row_start[b], 0), a.max_rows), hi = min(max(a.row_start[b + 1], 0), a.max_rows);
+  const int rows = max(hi - lo, 0);
+  s.row0 = lo;
+  s.nq = rows * (a.n_heads / a.pages.n_kv_heads);
+  s.tiles = (s.nq + R - 1) / R;
+  s.tq = s.tiles ? ((s.nq + s.tiles - 1) / s.tiles + 7) / 8 * 8 : 0;
+  const long long cap = (long long)a.max_pages * a.pages.page_size;
+  const int n = max(a.kv_len[b], 0);
+  if (n > cap && rows && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+  s.nk = (int)min((long long)n, cap);
+  s.nblk = max(1, (int)(((long long)s.nk + KB - 1) / KB));  // an empty sequence still gets its zeros
+  return s;
+}
+
+// A place in the line of units: block blk of (b, kv head, tile).
+struct Place {
+  int b, kvh, tile, blk;
+  Seq s;
+};
+template <int R, int KB>
+__device__ __forceinline__ void next_seq(const PagedAttnArgs &a, Place &p) {
+  while (++p.b < a.B) {
+    p.s = seq_of<R, KB>(a, p.b);
+    if (p.s.tiles) break;
   }
+}
+template <int R, int KB>
+__device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n) {
+  p.blk += n;
+  while (p.b < a.B && p.blk >= p.s.nblk) {
+    p.blk -= p.s.nblk;
+    if (++p.tile == p.s.tiles) {
+      p.tile = 0;
+      if (++p.kvh == a.pages.n_kv_heads) {
+        p.kvh = 0;
+        next_seq<R, KB>(a, p);
+      }
+    }
+  }
+}
+
+template <int DP, bool F32>
+__global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
+    k_paged_attn(const __grid_constant__ PagedAttnArgs a, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+                 Share *__restrict__ shares) {
+  using C = Cfg<DP, F32>;
+  constexpr int KB = C::kKB, W = C::kW, NT = C::kNT, R = C::kR, NST = C::kNst;
+  constexpr int CPR = C::kRow / 16;  // 16-byte chunks of a key row
+  pdl_enter();
+  extern __shared__ __align__(16) uint8_t sm_raw[];
+  __shared__ long long s_scan[32];
+  __shared__ Place s_place;
+  __shared__ uint32_t s_mask[W][NST];
+  __shared__ float2 s_ml[W][R];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int hd = a.pages.head_dim, KV = a.pages.n_kv_heads, G = a.n_heads / KV;
+
+  // ---- this CTA's range [u0, u1) of the units and its first place
+  long long u0, u1, total;
+  int ranges;
+  {
+    const int per = (a.B + C::kThreads - 1) / C::kThreads;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_of<R, KB>(a, b).units(KV);
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    __syncthreads();
+    long long base = 0;
+    total = 0;
+    for (int i = 0; i < W; ++i) {
+      if (i == warp) base = total;
+      total += s_scan[i];
+    }
+    // at least one block per warp in a range
+    ranges = (int)min((long long)gridDim.x, (total + W - 1) / W);
+    if ((int)blockIdx.x >= ranges) {
+      if (tid == 0) shares[blockIdx.x].last = -1;
+      return;
+    }
+    u0 = total * blockIdx.x / ranges;
+    u1 = total * (blockIdx.x + 1) / ranges;
+    long long at = base + x - mine;
+    if (u0 >= at && u0 < at + mine) {  // exactly one thread
+      Place p;
+      for (p.b = b0; p.b < b1; ++p.b) {
+        p.s = seq_of<R, KB>(a, p.b);
+        if (u0 < at + p.s.units(KV)) break;
+        at += p.s.units(KV);
+      }
+      const long long off = u0 - at;
+      const long long item = off / p.s.nblk;
+      p.blk = (int)(off - item * p.s.nblk);
+      p.kvh = (int)(item / p.s.tiles);
+      p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
+      s_place = p;
+    }
+    __syncthreads();
+  }
+  Place seg = s_place;  // start of the current segment (the part of an item inside the range)
+
+  uint8_t *sm = sm_raw;
+  const uint32_t ring = su32(sm) + (uint32_t)(warp * NST * C::kStage);
+  uint8_t *q_sm = sm + C::kRing;
+  float *red = reinterpret_cast<float *>(sm + C::kRing + C::kQ);  // [W / 2][DP][8]
+  [[maybe_unused]] float *p_sm = reinterpret_cast<float *>(sm + C::kRing + C::kQ + C::kRed) + warp * 64;
+
+  // ---- the warp's loader: blocks u0 + warp, + W, ...
+  Place ld = seg;
+  advance<R, KB>(a, ld, warp);
+  long long ld_u = u0 + warp;
+  int ld_pg = -1;  // page of this lane's key of the block to be loaded
+  auto fetch_page = [&]() {
+    ld_pg = -1;
+    const int key = ld.blk * KB + lane;
+    if (ld_u < u1 && lane < KB && key < ld.s.nk)
+      ld_pg = a.table[(size_t)ld.b * a.max_pages + (unsigned)key / (unsigned)a.pages.page_size];
+  };
+  auto issue = [&](int st) {
+    if (ld_u < u1) {
+      const int key = ld.blk * KB + lane;
+      const bool in = lane < KB && key < ld.s.nk;
+      const bool ok = in && ld_pg >= 0 && ld_pg < a.pages.n_pages;
+      if (in && !ok && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+      long long off = 0;
+      if (ok)
+        off = (long long)ld_pg * a.pages.page_stride +
+              (long long)((unsigned)key % (unsigned)a.pages.page_size) * a.pages.slot_stride +
+              (long long)ld.kvh * a.pages.head_stride;
+      const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) s_mask[warp][st] = mask;
+      const uint32_t dst = ring + (uint32_t)(st * C::kStage);
+      const char *kb = static_cast<const char *>(a.pages.k), *vb = static_cast<const char *>(a.pages.v);
+#pragma unroll
+      for (int i = 0; i < KB * CPR / 32; ++i) {
+        const int r = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
+        const long long o = __shfl_sync(0xffffffffu, off, r);
+        const bool v = ((mask >> r) & 1u) && c * (16 / C::kEs) < hd;
+        const long long byte = v ? o * C::kEs + c * 16 : 0;
+        const uint32_t d = dst + (uint32_t)(r * C::kRow) + (swz<F32>(r, c) << 4);
+        cpa16(d, kb + byte, v);
+        cpa16(d + (uint32_t)(KB * C::kRow), vb + byte, v);
+      }
+      ld_u += W;
+      if (ld_u < u1) advance<R, KB>(a, ld, W);
+      fetch_page();
+    }
+    cpa_commit();
+  };
+  fetch_page();
+  for (int i = 0; i < NST - 1; ++i) issue(i);
+  int st_load = NST - 1, st_use = 0;
+
+  // ---- segments
+  long long u = u0 + warp;  // the warp's next unit
+  for (long long s0 = u0; s0 < u1;) {
+    const Seq &sq = seg.s;
+    const long long s1 = min(u1, s0 + (sq.nblk - seg.blk));
+    const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
+    const int ngrp = (nq + 7) >> 3;
+    // queries of the tile -> shared memory (zeros past nq and past head_dim)
+    {
+      const char *qb = static_cast<const char *>(a.q);
+      for (int i = tid; i < ngrp * 8 * CPR; i += C::kThreads) {
+        const int r = i / CPR, c = i - r * CPR;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < nq && c * (16 / C::kEs) < hd) {
+          const int pq = q0 + r, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+          v = *reinterpret_cast<const uint4 *>(qb + ((size_t)row * a.n_heads + h) * hd * C::kEs + c * 16);
+        }
+        *reinterpret_cast<uint4 *>(q_sm + r * C::kQPitch + c * 16) = v;
+      }
+    }
+    __syncthreads();
+
+    float m_run[NT][2], l_run[NT][2];
+    float o[NT][C::kAcc][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m_run[n][0] = m_run[n][1] = -INFINITY;
+      l_run[n][0] = l_run[n][1] = 0.f;
+#pragma unroll
+      for (auto &x : o[n]) x[0] = x[1] = x[2] = x[3] = 0.f;
+    }
+
+    for (; u < s1; u += W) {
+      cpa_wait<NST - 2>();
+      __syncwarp();
+      issue(st_load);
+      st_load = st_load + 1 == NST ? 0 : st_load + 1;
+      const uint32_t kt = ring + (uint32_t)(st_use * C::kStage), vt = kt + (uint32_t)(KB * C::kRow);
+      const uint32_t mask = s_mask[warp][st_use];
+      st_use = st_use + 1 == NST ? 0 : st_use + 1;
+      if constexpr (!F32) {
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+        // S^T[key][query]: A = K (16 keys x 16 dims), B = Q^T
+#pragma unroll
+        for (int kk = 0; kk < DP / 32; ++kk) {
+          uint32_t ka[2][4];
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = 4 * kk + 2 * h2 + (lane >> 4);
+            ldsm4(kt + (uint32_t)(r * C::kRow) + (swz<false>(r, c) << 4), ka[h2]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n < ngrp) {
+              uint32_t qa[4];  // dims 32 kk + 8 i of the 8 queries
+              ldsm4(su32(q_sm) + (uint32_t)((n * 8 + (lane & 7)) * C::kQPitch + (4 * kk + (lane >> 3)) * 16), qa);
+              mma16816(s[n], ka[0], qa[0], qa[1]);
+              mma16816(s[n], ka[1], qa[2], qa[3]);
+            }
+          }
+        }
+        uint32_t ph[NT][2], pl[NT][2];
+        const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (n < ngrp) {
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = (e < 2 ? v0 : v1) ? s[n][e] * a.scale_log2 : -INFINITY;
+            float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+            for (int of = 4; of < 32; of <<= 1) {
+              mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], of));
+              mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], of));
+            }
+            // The maximum moves only when a block exceeds it by more than 8 (log2 units), so P stays below 2^8 and
+            // most blocks rescale nothing; O, the sum and P share it, so the result is the same.
+            const bool grow = mx[0] > m_run[n][0] + 8.f || mx[1] > m_run[n][1] + 8.f;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const float m2 = fmaxf(m_run[n][c], mx[c]);
+                const float f = m_run[n][c] == -INFINITY ? 0.f : exp2f(m_run[n][c] - m2);
+                m_run[n][c] = m2;
+                l_run[n][c] *= f;
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i) {
+                  o[n][i][c] *= f;
+                  o[n][i][c + 2] *= f;
+                }
+              }
+            }
+            float p[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float m = m_run[n][e & 1];
+              p[e] = exp2f(x[e] - (m == -INFINITY ? 0.f : m));
+              lo[e] = p[e] - __bfloat162float(__float2bfloat16_rn(p[e]));
+            }
+            l_run[n][0] += p[0] + p[2];
+            l_run[n][1] += p[1] + p[3];
+            ph[n][0] = movm(pack2(p[0], p[1]));
+            ph[n][1] = movm(pack2(p[2], p[3]));
+            pl[n][0] = movm(pack2(lo[0], lo[1]));
+            pl[n][1] = movm(pack2(lo[2], lo[3]));
+          }
+        }
+        // O^T[dim][query] += V^T P^T: A = V^T (16 dims x 16 keys)
+#pragma unroll
+        for (int i = 0; i < DP / 16; ++i) {
+          uint32_t va[4];
+          const int r = (lane & 7) + (lane >> 4) * 8, c = 2 * i + ((lane >> 3) & 1);
+          ldsm4t(vt + (uint32_t)(r * C::kRow) + (swz<false>(r, c) << 4), va);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n < ngrp) {
+              mma16816(o[n][i], va, ph[n][0], ph[n][1]);
+              mma16816(o[n][i], va, pl[n][0], pl[n][1]);
+            }
+          }
+        }
+      } else {
+        // lane = (key g, quarter t): its quarter of the 16-byte chunks of the row, all 8 queries
+        const uint8_t *kr = sm + (kt - su32(sm)) + g * C::kRow;
+        float s[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) s[r] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < CPR / 4; ++i) {
+          const int c = 4 * i + t;
+          const float4 kv = *reinterpret_cast<const float4 *>(kr + (swz<true>(g, c) << 4));
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float4 qv = *reinterpret_cast<const float4 *>(q_sm + r * C::kQPitch + c * 16);
+            s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+          }
+        }
+        float x[2];
+        const bool v = (mask >> g) & 1u;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {  // the lane's queries 2 t, 2 t + 1
+          const float sv = t == 0 ? s[c] : t == 1 ? s[2 + c] : t == 2 ? s[4 + c] : s[6 + c];
+          x[c] = v ? sv * a.scale_log2 : -INFINITY;
+        }
+        float mx[2] = {x[0], x[1]};
+#pragma unroll
+        for (int of = 4; of < 32; of <<= 1) {
+          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], of));
+          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], of));
+        }
+        const bool grow = mx[0] > m_run[0][0] + 8.f || mx[1] > m_run[0][1] + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float m2 = fmaxf(m_run[0][c], mx[c]);
+            f[c] = m_run[0][c] == -INFINITY ? 0.f : exp2f(m_run[0][c] - m2);
+            m_run[0][c] = m2;
+            l_run[0][c] *= f[c];
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float fr = __shfl_sync(0xffffffffu, f[r & 1], r >> 1);
+#pragma unroll
+            for (int i = 0; i < C::kND; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[0][r * C::kND + i][e] *= fr;
+          }
+        }
+        float p[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          p[c] = exp2f(x[c] - (m_run[0][c] == -INFINITY ? 0.f : m_run[0][c]));
+          l_run[0][c] += p[c];
+        }
+        __syncwarp();
+        *reinterpret_cast<float2 *>(p_sm + g * 8 + 2 * t) = make_float2(p[0], p[1]);
+        __syncwarp();
+        // O: the lane's chunk(s) of the head dim; DP == 64: half a warp takes every other key
+        constexpr int ND = C::kND, KS = DP == 64 ? 2 : 1;
+        const uint8_t *vr = sm + (vt - su32(sm));
+#pragma unroll
+        for (int k2 = 0; k2 < KB / KS; ++k2) {
+          const int key = KS == 2 ? 2 * k2 + (lane >> 4) : k2;
+          const float4 pa = *reinterpret_cast<const float4 *>(p_sm + key * 8);
+          const float4 pb = *reinterpret_cast<const float4 *>(p_sm + key * 8 + 4);
+          const float pr[8] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
+#pragma unroll
+          for (int i = 0; i < ND; ++i) {
+            const int c = (KS == 2 ? (lane & 15) : lane) + 32 * i;
+            const float4 vv = *reinterpret_cast<const float4 *>(vr + key * C::kRow + (swz<true>(key, c) << 4));
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+              float(&od)[4] = o[0][r * ND + i];
+              od[0] = fmaf(pr[r], vv.x, od[0]);
+              od[1] = fmaf(pr[r], vv.y, od[1]);
+              od[2] = fmaf(pr[r], vv.z, od[2]);
+              od[3] = fmaf(pr[r], vv.w, od[3]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the segment's end: join the warps
+    const bool starts = seg.blk == 0, ends = s1 - s0 == sq.nblk - seg.blk;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float l = l_run[n][c];
+#pragma unroll
+        for (int of = 4; of < 32; of <<= 1) l += __shfl_xor_sync(0xffffffffu, l, of);
+        l_run[n][c] = l;
+        if (g == 0) s_ml[warp][n * 8 + 2 * t + c] = make_float2(m_run[n][c], l);
+      }
+    __syncthreads();
+    const int slot = s0 == u0 ? 0 : 1;  // the range's first segment, or its last one
+    const size_t pbase = ((size_t)blockIdx.x * 2 + slot) * R;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (n < ngrp) {
+        // factor of this warp's share of queries 8 n + 2 t, + 1
+        float f[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w2 = 0; w2 < W; ++w2) M = fmaxf(M, s_ml[w2][n * 8 + 2 * t + c].x);
+          f[c] = m_run[n][c] == -INFINITY ? 0.f : exp2f(m_run[n][c] - M);
+        }
+        if constexpr (!F32) {
+#pragma unroll
+          for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][i][e] *= f[e & 1];
+        } else {
+          constexpr int ND = C::kND;
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            const float fr = __shfl_sync(0xffffffffu, f[r & 1], r >> 1);
+#pragma unroll
+            for (int i = 0; i < ND; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float x = o[0][r * ND + i][e] * fr;
+                if (DP == 64) x += __shfl_xor_sync(0xffffffffu, x, 16);
+                o[0][r * ND + i][e] = x;
+              }
+          }
+        }
+        // the upper half of the warps hands its shares to the lower half, whose W / 2 sums stay in the buffer
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          if ((warp >= W / 2) == (half == 1)) {
+            float *bw = red + (size_t)(warp % (W / 2)) * DP * 8;  // [dim][8 queries]
+            if constexpr (!F32) {
+#pragma unroll
+              for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float2 *d = reinterpret_cast<float2 *>(bw + (i * 16 + g + 8 * e) * 8 + 2 * t);
+                  float2 v = make_float2(o[n][i][2 * e], o[n][i][2 * e + 1]);
+                  if (half == 0) {
+                    const float2 w2 = *d;
+                    v.x += w2.x;
+                    v.y += w2.y;
+                  }
+                  *d = v;
+                }
+            } else {
+              constexpr int ND = C::kND;
+              if (DP != 64 || lane < 16) {
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    float4 *d = reinterpret_cast<float4 *>(bw + ((lane + 32 * i) * 4 + e) * 8);
+#pragma unroll
+                    for (int r4 = 0; r4 < 2; ++r4) {
+                      float4 v = make_float4(o[0][(4 * r4) * ND + i][e], o[0][(4 * r4 + 1) * ND + i][e],
+                                             o[0][(4 * r4 + 2) * ND + i][e], o[0][(4 * r4 + 3) * ND + i][e]);
+                      if (half == 0) {
+                        const float4 w2 = d[r4];
+                        v.x += w2.x;
+                        v.y += w2.y;
+                        v.z += w2.z;
+                        v.w += w2.w;
+                      }
+                      d[r4] = v;
+                    }
+                  }
+              }
+            }
+          }
+          __syncthreads();
+        }
+        // sum of the W / 2 buffers: whole items are normalised and stored, cut ones go to the workspace
+        for (int i = tid; i < DP * 8 / 2; i += C::kThreads) {
+          const int qr = i & 7, d = (i >> 3) * 2;
+          if (n * 8 + qr >= nq || d >= hd) continue;
+          float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+          for (int w2 = 0; w2 < W / 2; ++w2) {
+            x0 += red[(size_t)w2 * DP * 8 + d * 8 + qr];
+            x1 += red[(size_t)w2 * DP * 8 + (d + 1) * 8 + qr];
+          }
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int w2 = 0; w2 < W; ++w2) M = fmaxf(M, s_ml[w2][n * 8 + qr].x);
+#pragma unroll
+          for (int w2 = 0; w2 < W; ++w2) {
+            const float2 ml = s_ml[w2][n * 8 + qr];
+            L += ml.x == -INFINITY ? 0.f : ml.y * exp2f(ml.x - M);
+          }
+          if (starts && ends) {
+            const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+            const int pq = q0 + n * 8 + qr, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+            const size_t at = ((size_t)row * a.n_heads + h) * hd + d;
+            if constexpr (F32)
+              *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(x0 * inv, x1 * inv);
+            else
+              *reinterpret_cast<uint32_t *>(static_cast<bf16 *>(a.out) + at) = pack2(x0 * inv, x1 * inv);
+          } else {
+            *reinterpret_cast<float2 *>(part_o + (pbase + n * 8 + qr) * DP + d) = make_float2(x0, x1);
+            if (d == 0) part_ml[pbase + n * 8 + qr] = make_float2(M, L);
+          }
+        }
+        if (n + 1 < NT) __syncthreads();
+      }
+    }
+    if (s1 == u1 && tid == 0) {
+      Share sh;
+      sh.last = -1;
+      if (starts && !ends) {
+        // the range that holds the item's last unit
+        const long long last_u = s0 + sq.nblk - 1;
+        sh.last = (int)(((last_u + 1) * ranges + total - 1) / total) - 1;
+        sh.row0 = sq.row0;
+        sh.q0 = q0;
+        sh.nq = nq;
+        sh.kvh = seg.kvh;
+        sh.slot = slot;
+      }
+      shares[blockIdx.x] = sh;
+    }
+    advance<R, KB>(a, seg, (int)(s1 - s0));
+    s0 = s1;
+    __syncthreads();  // the next segment reuses the query tile, the sums and the buffer
+  }
+  cpa_wait<0>();
+}
+
+// Joins the shares of the item that begins in range blockIdx.x and ends in a
+// later one: shares in range order, w_i = 2^(m_i - M) / sum_i 2^(m_i - M) l_i.
+// The owner's share is its last segment (slot 1, or 0 when that is its only
+// one); the following ranges hold theirs in slot 0.  One warp per query.
+template <int DP, class T>
+__global__ void __launch_bounds__(256)
+    k_paged_merge(const __grid_constant__ PagedAttnArgs a, int R, const float *__restrict__ part_o,
+                  const float2 *__restrict__ part_ml, const Share *__restrict__ shares) {
+  pdl_enter();
+  const Share sh = shares[blockIdx.x];
+  if (sh.last < 0) return;
+  const int lane = threadIdx.x & 31;
+  const int G = a.n_heads / a.pages.n_kv_heads, hd = a.pages.head_dim;
+  const int first = blockIdx.x;
+  for (int qr = blockIdx.y * 8 + (threadIdx.x >> 5); qr < sh.nq; qr += gridDim.y * 8) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = first + lane; i <= sh.last; i += 32)
+      M = fmaxf(M, part_ml[((size_t)i * 2 + (i == first ? sh.slot : 0)) * R + qr].x);
+    M = warp_max(M);
+    float acc[DP / 32];
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = first; i <= sh.last; ++i) {
+      const size_t at = ((size_t)i * 2 + (i == first ? sh.slot : 0)) * R + qr;
+      const float2 ml = part_ml[at];
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      L += ml.x == -INFINITY ? 0.f : ml.y * w;
+#pragma unroll
+      for (int e = 0; e < DP / 32; ++e) {
+        const int d = lane + 32 * e;
+        if (d < hd) acc[e] += w * part_o[at * DP + d];
+      }
+    }
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
+    const int pq = sh.q0 + qr, row = sh.row0 + pq / G, h = sh.kvh * G + pq % G;
+#pragma unroll
+    for (int e = 0; e < DP / 32; ++e) {
+      const int d = lane + 32 * e;
+      if (d < hd) static_cast<T *>(a.out)[((size_t)row * a.n_heads + h) * hd + d] = from_f<T>(acc[e] * inv);
+    }
+  }
+}
+
+// Workspace: shares' O, (max, sum), descriptors; two shares per range at most.
+template <int DP, bool F32>
+constexpr int64_t ws_bytes() {
+  return (int64_t)kMaxRanges * 2 * Cfg<DP, F32>::kR * (DP * 4 + 8) + (int64_t)kMaxRanges * sizeof(Share);
+}
+
+template <int DP, bool F32>
+cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  using C = Cfg<DP, F32>;
+  using T = std::conditional_t<F32, float, bf16>;
+  static std::atomic<uint64_t> attr{0};
+  if (cudaError_t e = ensure_smem_limit(k_paged_attn<DP, F32>, C::kSmem, attr)) return e;
+  int dev = 0, sms = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+  const int grid = sms < kMaxRanges ? sms : kMaxRanges;
+  float *part_o = static_cast<float *>(ws);
+  float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)kMaxRanges * 2 * C::kR * DP);
+  Share *shares = reinterpret_cast<Share *>(part_ml + (size_t)kMaxRanges * 2 * C::kR);
+  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, part_o, part_ml,
+                                 shares))
+    return e;
+  return launch_pdl(k_paged_merge<DP, T>, dim3(grid, C::kR / 8), dim3(256), 0, s, a, C::kR, part_o, part_ml, shares);
 }
 
 }  // namespace
 
-int64_t paged_attention_workspace(const dcu_pages &) { return 16; }
+int64_t paged_attention_workspace(const dcu_pages &p) {
+  const bool f = p.dtype == DCU_F32;
+  if (p.head_dim <= 64) return f ? ws_bytes<64, true>() : ws_bytes<64, false>();
+  if (p.head_dim <= 128) return f ? ws_bytes<128, true>() : ws_bytes<128, false>();
+  return f ? ws_bytes<256, true>() : ws_bytes<256, false>();
+}
 
-cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *, cudaStream_t s) {
-  const long long items = (long long)a.max_rows * a.n_heads;
-  const int grid = (int)(items / 4 + 1 < 148 * 16 ? items / 4 + 1 : 148 * 16);
-  if (a.pages.dtype == DCU_BF16) launch_pdl(k_paged_attn_rowhead<bf16>, dim3(grid), dim3(128), 0, s, a);
-  else launch_pdl(k_paged_attn_rowhead<float>, dim3(grid), dim3(128), 0, s, a);
-  return cudaGetLastError();
+cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  const bool f = a.pages.dtype == DCU_F32;
+  if (a.pages.head_dim <= 64) return f ? launch<64, true>(a, ws, s) : launch<64, false>(a, ws, s);
+  if (a.pages.head_dim <= 128) return f ? launch<128, true>(a, ws, s) : launch<128, false>(a, ws, s);
+  return f ? launch<256, true>(a, ws, s) : launch<256, false>(a, ws, s);
 }
 
 }  // namespace dcu
