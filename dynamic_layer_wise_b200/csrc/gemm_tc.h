@@ -158,6 +158,10 @@ struct TcParams {
 // missing or the encoding is rejected.
 bool encode_tmap_bf16(CUtensorMap *map, const void *ptr, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                       uint32_t box_inner, uint32_t box_outer);
+// 4-D map (bf16 or float32, 128-byte swizzle, box[0] elements of 128 bytes);
+// false when the driver refuses the geometry.
+bool encode_tmap_4d(CUtensorMap *map, bool f32, const void *ptr, const uint64_t (&dims)[4],
+                    const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4]);
 // bn: token rows per pass (128 or 256); the grid is p.ph[0].geo.grid CTAs (a
 // cooperative launch when p.chain).
 cudaError_t launch_gemm_tc(TcParams p, int bn, cudaStream_t s);

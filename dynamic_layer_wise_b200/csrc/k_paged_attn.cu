@@ -28,8 +28,9 @@
 // blocks run on the CUDA cores in fp32.
 #include <type_traits>
 
-#include "common.cuh"
+#include "gemm_tc.h"
 #include "paged.h"
+#include "tc_ptx.cuh"
 
 namespace dcu {
 namespace {
@@ -37,12 +38,11 @@ namespace {
 constexpr int kMaxRanges = 148;  // most CTAs (work ranges) of a launch
 
 // One kernel variant: head dims up to DP (shorter ones zero-padded in shared memory).
-template <int DP, bool F32>
+template <int DP, bool F32, int NT>
 struct Cfg {
   static constexpr int kKB = F32 ? 8 : 16;                       // keys of a block
   static constexpr int kW = DP == 256 ? 4 : 8;                   // warps
-  static constexpr int kNT = F32 ? 1 : (DP == 256 ? 2 : 4);      // groups of 8 queries in a tile
-  static constexpr int kR = 8 * kNT;                             // queries of a tile
+  static constexpr int kR = 8 * NT;                              // queries of a tile: NT groups of 8
   static constexpr int kEs = F32 ? 4 : 2;                        // element size
   static constexpr int kRow = DP * kEs;                          // bytes of a key row
   static constexpr int kStage = 2 * kKB * kRow;                  // K and V of a block
@@ -52,7 +52,7 @@ struct Cfg {
   static constexpr int kQ = kR * kQPitch;
   static constexpr int kRed = (kW / 2) * DP * 8 * 4;             // merge buffer: half the warps, 8 queries
   static constexpr int kP = F32 ? kW * 64 * 4 : 0;               // float32: P of a block, per warp
-  static constexpr int kSmem = kRing + kQ + kRed + kP + 16;
+  static constexpr int kSmem = kRing + kQ + kRed + kP + 1024;  // + alignment of the ring
   static constexpr int kThreads = 32 * kW;
   static constexpr int kND = F32 ? (DP > 128 ? DP / 128 : 1) : 0;  // float32: 4-dim chunks of O per lane and query
   static constexpr int kAcc = F32 ? 8 * kND : DP / 16;           // float4s of O per lane and query group
@@ -107,12 +107,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// 16-byte chunk c of key row r: bits of r spread the rows that are read
-// together over the banks (bf16: the 8 rows of an ldmatrix; float32: the two
-// key rows of a quarter warp).
-template <bool F32>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  return F32 ? (uint32_t)(c ^ (((r & 1) << 2) | ((r >> 1) & 3))) : (uint32_t)(c ^ (r & 7));
+// 2^x; results below 2^-126 become 0 (they round away in every sum here)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// key / page_size: a shift for the usual powers of two
+__device__ __forceinline__ unsigned div_page(const PagedAttnArgs &a, unsigned key) {
+  return a.page_shift >= 0 ? key >> a.page_shift : key / (unsigned)a.pages.page_size;
 }
 
 // The items of sequence b.
@@ -164,22 +167,54 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n)
   }
 }
 
-template <int DP, bool F32>
-__global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
-    k_paged_attn(const __grid_constant__ PagedAttnArgs a, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+// 16-byte chunk c of key row r in a block's K or V: boxes of KB rows x 128
+// bytes with the 128-byte swizzle (the layout that a TMA tile load writes).
+template <int KB>
+__device__ __forceinline__ uint32_t kv_off(int r, int c) {
+  return (uint32_t)((c >> 3) * (KB * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// A block to be loaded: its page (TMA: one page; cp.async: the page of the
+// lane's key), the slot offset of its first key, kv head and valid keys.
+struct Req {
+  int pg, blk, kvh, nk;
+};
+
+template <int DP, bool F32, int NT, bool TMA>
+__global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
+    k_paged_attn(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap, int head_first, float *__restrict__ part_o, float2 *__restrict__ part_ml,
                  Share *__restrict__ shares) {
-  using C = Cfg<DP, F32>;
-  constexpr int KB = C::kKB, W = C::kW, NT = C::kNT, R = C::kR, NST = C::kNst;
+  using C = Cfg<DP, F32, NT>;
+  constexpr int KB = C::kKB, W = C::kW, R = C::kR, NST = C::kNst;
   constexpr int CPR = C::kRow / 16;  // 16-byte chunks of a key row
+  constexpr uint32_t FULL = (1u << KB) - 1u;
   pdl_enter();
-  extern __shared__ __align__(16) uint8_t sm_raw[];
+  extern __shared__ uint8_t sm_raw[];
   __shared__ long long s_scan[32];
   __shared__ Place s_place;
   __shared__ uint32_t s_mask[W][NST];
   __shared__ float2 s_ml[W][R];
+  __shared__ __align__(8) uint64_t s_bar[W][NST];
+  __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int hd = a.pages.head_dim, KV = a.pages.n_kv_heads, G = a.n_heads / KV;
+  if (TMA) fence_proxy_async_global();  // the pages may have been written by the kernel just waited for
+  if (TMA && tid == 0) {
+    for (int i = 0; i < W * NST; ++i) mbar_init(su32(&s_bar[0][0]) + 8u * i, 1);
+    fence_barrier_init();
+    s_abort = 0;
+  }
 
   // ---- this CTA's range [u0, u1) of the units and its first place
   long long u0, u1, total;
@@ -230,8 +265,10 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
   }
   Place seg = s_place;  // start of the current segment (the part of an item inside the range)
 
-  uint8_t *sm = sm_raw;
-  const uint32_t ring = su32(sm) + (uint32_t)(warp * NST * C::kStage);
+  uint8_t *sm = sm_raw + ((1024u - (su32(sm_raw) & 1023u)) & 1023u);
+  const uint32_t sm32 = su32(sm);
+  const uint32_t ring = sm32 + (uint32_t)(warp * NST * C::kStage);
+  const uint32_t bars = su32(&s_bar[warp][0]);
   uint8_t *q_sm = sm + C::kRing;
   float *red = reinterpret_cast<float *>(sm + C::kRing + C::kQ);  // [W / 2][DP][8]
   [[maybe_unused]] float *p_sm = reinterpret_cast<float *>(sm + C::kRing + C::kQ + C::kRed) + warp * 64;
@@ -240,47 +277,88 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
   Place ld = seg;
   advance<R, KB>(a, ld, warp);
   long long ld_u = u0 + warp;
-  int ld_pg = -1;  // page of this lane's key of the block to be loaded
-  auto fetch_page = [&]() {
-    ld_pg = -1;
-    const int key = ld.blk * KB + lane;
-    if (ld_u < u1 && lane < KB && key < ld.s.nk)
-      ld_pg = a.table[(size_t)ld.b * a.max_pages + (unsigned)key / (unsigned)a.pages.page_size];
-  };
-  auto issue = [&](int st) {
+  const unsigned psz = (unsigned)a.pages.page_size;
+  // the next block of this warp: starts the look-up of its page(s), which `issue` uses later
+  auto request = [&]() {
+    Req r{-1, 0, 0, 0};
     if (ld_u < u1) {
-      const int key = ld.blk * KB + lane;
-      const bool in = lane < KB && key < ld.s.nk;
-      const bool ok = in && ld_pg >= 0 && ld_pg < a.pages.n_pages;
+      r.blk = ld.blk;
+      r.kvh = ld.kvh;
+      r.nk = ld.s.nk;
+      const int key = ld.blk * KB + (TMA ? 0 : lane);
+      if (key < r.nk && (TMA || lane < KB))
+        r.pg = a.table[(size_t)ld.b * a.max_pages + div_page(a, (unsigned)key)];
+      ld_u += W;
+      if (ld_u < u1) advance<R, KB>(a, ld, W);
+    }
+    return r;
+  };
+  auto issue = [&](const Req &r, int st) {
+    const uint32_t dst = ring + (uint32_t)(st * C::kStage);
+    const int key0 = r.blk * KB;
+    if constexpr (TMA) {
+      const int nv = min(KB, r.nk - key0);  // <= 0: nothing to load
+      const bool ok = nv > 0 && r.pg >= 0 && r.pg < a.pages.n_pages;
+      if (lane == 0) {
+        s_mask[warp][st] = ok ? FULL >> (KB - nv) : 0u;
+        const uint32_t bar = bars + 8u * st;
+        mbar_expect_tx(bar, ok ? (uint32_t)C::kStage : 0u);
+        if (ok) {
+          const int y = key0 - (int)(div_page(a, (unsigned)key0) * psz);
+#pragma unroll
+          for (int i = 0; i < CPR / 8; ++i) {
+            const int x = i * (128 / C::kEs), c1 = head_first ? r.kvh : y, c2 = head_first ? y : r.kvh;
+            tma_load_4d(dst + (uint32_t)(i * KB * 128), &kmap, x, c1, c2, r.pg, bar);
+            tma_load_4d(dst + (uint32_t)(KB * C::kRow + i * KB * 128), &vmap, x, c1, c2, r.pg, bar);
+          }
+        } else if (nv > 0 && a.status) {
+          atomicOr(a.status, DCU_ST_BAD_PAGE);
+        }
+      }
+    } else {
+      const int key = key0 + lane;
+      const bool in = lane < KB && key < r.nk;
+      const bool ok = in && r.pg >= 0 && r.pg < a.pages.n_pages;
       if (in && !ok && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
       long long off = 0;
       if (ok)
-        off = (long long)ld_pg * a.pages.page_stride +
-              (long long)((unsigned)key % (unsigned)a.pages.page_size) * a.pages.slot_stride +
-              (long long)ld.kvh * a.pages.head_stride;
+        off = (long long)r.pg * a.pages.page_stride +
+              (long long)((unsigned)key - div_page(a, (unsigned)key) * psz) * a.pages.slot_stride +
+              (long long)r.kvh * a.pages.head_stride;
       const uint32_t mask = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) s_mask[warp][st] = mask;
-      const uint32_t dst = ring + (uint32_t)(st * C::kStage);
       const char *kb = static_cast<const char *>(a.pages.k), *vb = static_cast<const char *>(a.pages.v);
 #pragma unroll
       for (int i = 0; i < KB * CPR / 32; ++i) {
-        const int r = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
-        const long long o = __shfl_sync(0xffffffffu, off, r);
-        const bool v = ((mask >> r) & 1u) && c * (16 / C::kEs) < hd;
+        const int rr = (i * 32 + lane) / CPR, c = (i * 32 + lane) % CPR;
+        const long long o = __shfl_sync(0xffffffffu, off, rr);
+        const bool v = ((mask >> rr) & 1u) && c * (16 / C::kEs) < hd;
         const long long byte = v ? o * C::kEs + c * 16 : 0;
-        const uint32_t d = dst + (uint32_t)(r * C::kRow) + (swz<F32>(r, c) << 4);
+        const uint32_t d = dst + kv_off<KB>(rr, c);
         cpa16(d, kb + byte, v);
         cpa16(d + (uint32_t)(KB * C::kRow), vb + byte, v);
       }
-      ld_u += W;
-      if (ld_u < u1) advance<R, KB>(a, ld, W);
-      fetch_page();
+      cpa_commit();
     }
-    cpa_commit();
   };
-  fetch_page();
-  for (int i = 0; i < NST - 1; ++i) issue(i);
+  int left = (int)max(0ll, (u1 - u0 - warp + W - 1) / W);  // blocks of this warp not yet asked for
+  Req nxt{};
+  {
+    Req first[NST - 1];
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) first[i] = request();
+    nxt = request();
+#pragma unroll
+    for (int i = 0; i < NST - 1; ++i) {
+      if (i < left) issue(first[i], i);
+      else if (!TMA) cpa_commit();
+    }
+    left -= NST - 1;
+  }
   int st_load = NST - 1, st_use = 0;
+  uint32_t parity = 0;
+  [[maybe_unused]] bool alive = true;
+  [[maybe_unused]] int undone = 0;  // blocks issued but not waited for
 
   // ---- segments
   long long u = u0 + warp;  // the warp's next unit
@@ -288,7 +366,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
     const Seq &sq = seg.s;
     const long long s1 = min(u1, s0 + (sq.nblk - seg.blk));
     const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
-    const int ngrp = (nq + 7) >> 3;
+    const int ngrp = NT == 1 ? 1 : (nq + 7) >> 3;
     // queries of the tile -> shared memory (zeros past nq and past head_dim)
     {
       const char *qb = static_cast<const char *>(a.q);
@@ -303,6 +381,13 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
       }
     }
     __syncthreads();
+    // B fragments of a single query group stay in registers: dims 32 kk + 8 i of the 8 queries
+    [[maybe_unused]] uint32_t qf[F32 || NT > 1 ? 1 : DP / 32][4];
+    if constexpr (!F32 && NT == 1) {
+#pragma unroll
+      for (int kk = 0; kk < DP / 32; ++kk)
+        ldsm4(su32(q_sm) + (uint32_t)((lane & 7) * C::kQPitch + (4 * kk + (lane >> 3)) * 16), qf[kk]);
+    }
 
     float m_run[NT][2], l_run[NT][2];
     float o[NT][C::kAcc][4];
@@ -315,44 +400,85 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
     }
 
     for (; u < s1; u += W) {
-      cpa_wait<NST - 2>();
-      __syncwarp();
-      issue(st_load);
+      if constexpr (TMA) {
+        if (alive) {
+          alive = __all_sync(0xffffffffu, wait_bounded(bars + 8u * st_use, parity, &s_abort, a.status));
+          if (!alive) undone = min(NST - 1, left + NST - 1);
+        }
+        if (!alive) continue;  // the wait gave up (DCU_ST_TIMEOUT): nothing more is loaded or read
+      } else {
+        cpa_wait<NST - 2>();
+        __syncwarp();
+      }
+      if (left > 0) {  // the stage read in the last pass
+        issue(nxt, st_load);
+        nxt = request();
+      } else if (!TMA) {
+        cpa_commit();
+      }
+      --left;
       st_load = st_load + 1 == NST ? 0 : st_load + 1;
       const uint32_t kt = ring + (uint32_t)(st_use * C::kStage), vt = kt + (uint32_t)(KB * C::kRow);
       const uint32_t mask = s_mask[warp][st_use];
-      st_use = st_use + 1 == NST ? 0 : st_use + 1;
+      if (++st_use == NST) {
+        st_use = 0;
+        parity ^= 1u;
+      }
+      if (mask == 0u) {
+        __syncwarp();
+        continue;
+      }
+      if (TMA && mask != FULL) {
+        // past the sequence's end the page holds anything: P is 0 there, V must be
+        const int nv = __popc(mask);
+        for (int i = lane; i < (KB - nv) * CPR; i += 32)
+          *reinterpret_cast<uint4 *>(sm + (vt - sm32) + kv_off<KB>(nv + i / CPR, i % CPR)) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();  // before the stage's next TMA load
+        __syncwarp();
+      }
       if constexpr (!F32) {
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
         // S^T[key][query]: A = K (16 keys x 16 dims), B = Q^T
+        [[maybe_unused]] float s2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = 0; kk < DP / 32; ++kk) {
           uint32_t ka[2][4];
 #pragma unroll
-          for (int h2 = 0; h2 < 2; ++h2) {
-            const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = 4 * kk + 2 * h2 + (lane >> 4);
-            ldsm4(kt + (uint32_t)(r * C::kRow) + (swz<false>(r, c) << 4), ka[h2]);
-          }
+          for (int h2 = 0; h2 < 2; ++h2)
+            ldsm4(kt + kv_off<KB>((lane & 7) + ((lane >> 3) & 1) * 8, 4 * kk + 2 * h2 + (lane >> 4)), ka[h2]);
+          if constexpr (NT == 1) {  // two chains of products
+            mma16816(s[0], ka[0], qf[kk][0], qf[kk][1]);
+            mma16816(s2, ka[1], qf[kk][2], qf[kk][3]);
+          } else {
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n < ngrp) {
-              uint32_t qa[4];  // dims 32 kk + 8 i of the 8 queries
-              ldsm4(su32(q_sm) + (uint32_t)((n * 8 + (lane & 7)) * C::kQPitch + (4 * kk + (lane >> 3)) * 16), qa);
-              mma16816(s[n], ka[0], qa[0], qa[1]);
-              mma16816(s[n], ka[1], qa[2], qa[3]);
+            for (int n = 0; n < NT; ++n) {
+              if (n < ngrp) {
+                uint32_t qa[4];
+                ldsm4(su32(q_sm) + (uint32_t)((n * 8 + (lane & 7)) * C::kQPitch + (4 * kk + (lane >> 3)) * 16), qa);
+                mma16816(s[n], ka[0], qa[0], qa[1]);
+                mma16816(s[n], ka[1], qa[2], qa[3]);
+              }
             }
           }
         }
+        if constexpr (NT == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][e] += s2[e];
+        }
         uint32_t ph[NT][2], pl[NT][2];
-        const bool v0 = (mask >> g) & 1u, v1 = (mask >> (g + 8)) & 1u;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if (n < ngrp) {
             float x[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = (e < 2 ? v0 : v1) ? s[n][e] * a.scale_log2 : -INFINITY;
+            for (int e = 0; e < 4; ++e) x[e] = s[n][e] * a.scale_log2;
+            if (mask != FULL) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (!((mask >> (g + (e >> 1) * 8)) & 1u)) x[e] = -INFINITY;
+            }
             float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
 #pragma unroll
             for (int of = 4; of < 32; of <<= 1) {
@@ -366,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const float m2 = fmaxf(m_run[n][c], mx[c]);
-                const float f = m_run[n][c] == -INFINITY ? 0.f : exp2f(m_run[n][c] - m2);
+                const float f = m_run[n][c] == -INFINITY ? 0.f : ex2(m_run[n][c] - m2);
                 m_run[n][c] = m2;
                 l_run[n][c] *= f;
 #pragma unroll
@@ -380,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float m = m_run[n][e & 1];
-              p[e] = exp2f(x[e] - (m == -INFINITY ? 0.f : m));
+              p[e] = ex2(x[e] - (m == -INFINITY ? 0.f : m));
               lo[e] = p[e] - __bfloat162float(__float2bfloat16_rn(p[e]));
             }
             l_run[n][0] += p[0] + p[2];
@@ -395,8 +521,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < DP / 16; ++i) {
           uint32_t va[4];
-          const int r = (lane & 7) + (lane >> 4) * 8, c = 2 * i + ((lane >> 3) & 1);
-          ldsm4t(vt + (uint32_t)(r * C::kRow) + (swz<false>(r, c) << 4), va);
+          ldsm4t(vt + kv_off<KB>((lane & 7) + (lane >> 4) * 8, 2 * i + ((lane >> 3) & 1)), va);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n < ngrp) {
@@ -406,15 +531,16 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
           }
         }
       } else {
-        // lane = (key g, quarter t): its quarter of the 16-byte chunks of the row, all 8 queries
-        const uint8_t *kr = sm + (kt - su32(sm)) + g * C::kRow;
+        // lane = (key g, quarter t): its quarter of the 16-byte chunks of the row, all 8 queries; odd keys take the
+        // two halves of a 128-byte row in the other order, so a quarter warp's 8 chunks fall in 8 bank groups
+        const uint8_t *kr = sm + (kt - sm32);
         float s[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) s[r] = 0.f;
 #pragma unroll 4
         for (int i = 0; i < CPR / 4; ++i) {
-          const int c = 4 * i + t;
-          const float4 kv = *reinterpret_cast<const float4 *>(kr + (swz<true>(g, c) << 4));
+          const int c = 4 * (i ^ (g & 1)) + t;
+          const float4 kv = *reinterpret_cast<const float4 *>(kr + kv_off<KB>(g, c));
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
             const float4 qv = *reinterpret_cast<const float4 *>(q_sm + r * C::kQPitch + c * 16);
@@ -469,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
         __syncwarp();
         // O: the lane's chunk(s) of the head dim; DP == 64: half a warp takes every other key
         constexpr int ND = C::kND, KS = DP == 64 ? 2 : 1;
-        const uint8_t *vr = sm + (vt - su32(sm));
+        const uint8_t *vr = sm + (vt - sm32);
 #pragma unroll
         for (int k2 = 0; k2 < KB / KS; ++k2) {
           const int key = KS == 2 ? 2 * k2 + (lane >> 4) : k2;
@@ -479,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < ND; ++i) {
             const int c = (KS == 2 ? (lane & 15) : lane) + 32 * i;
-            const float4 vv = *reinterpret_cast<const float4 *>(vr + key * C::kRow + (swz<true>(key, c) << 4));
+            const float4 vv = *reinterpret_cast<const float4 *>(vr + kv_off<KB>(key, c));
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
               float(&od)[4] = o[0][r * ND + i];
@@ -491,6 +617,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
           }
         }
       }
+      __syncwarp();  // all lanes are done with the stage
     }
 
     // ---- the segment's end: join the warps
@@ -639,7 +766,17 @@ __global__ void __launch_bounds__(Cfg<DP, F32>::kThreads, 1)
     s0 = s1;
     __syncthreads();  // the next segment reuses the query tile, the sums and the buffer
   }
-  cpa_wait<0>();
+  if constexpr (TMA) {
+    for (int i = 0; i < undone; ++i) {  // after a timeout: no copy may land once the CTA has left
+      wait_drain(bars + 8u * st_use, parity);
+      if (++st_use == NST) {
+        st_use = 0;
+        parity ^= 1u;
+      }
+    }
+  } else {
+    cpa_wait<0>();
+  }
 }
 
 // Joins the shares of the item that begins in range blockIdx.x and ends in a
@@ -687,17 +824,18 @@ __global__ void __launch_bounds__(256)
 }
 
 // Workspace: shares' O, (max, sum), descriptors; two shares per range at most.
-template <int DP, bool F32>
+template <int DP, int NT>
 constexpr int64_t ws_bytes() {
-  return (int64_t)kMaxRanges * 2 * Cfg<DP, F32>::kR * (DP * 4 + 8) + (int64_t)kMaxRanges * sizeof(Share);
+  return (int64_t)kMaxRanges * 2 * 8 * NT * (DP * 4 + 8) + (int64_t)kMaxRanges * sizeof(Share);
 }
 
-template <int DP, bool F32>
-cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
-  using C = Cfg<DP, F32>;
+template <int DP, bool F32, int NT, bool TMA>
+cudaError_t launch_variant(const PagedAttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int head_first,
+                           void *ws, cudaStream_t s) {
+  using C = Cfg<DP, F32, NT>;
   using T = std::conditional_t<F32, float, bf16>;
   static std::atomic<uint64_t> attr{0};
-  if (cudaError_t e = ensure_smem_limit(k_paged_attn<DP, F32>, C::kSmem, attr)) return e;
+  if (cudaError_t e = ensure_smem_limit(k_paged_attn<DP, F32, NT, TMA>, C::kSmem, attr)) return e;
   int dev = 0, sms = 0;
   if (cudaError_t e = cudaGetDevice(&dev)) return e;
   if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
@@ -705,26 +843,68 @@ cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
   float *part_o = static_cast<float *>(ws);
   float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)kMaxRanges * 2 * C::kR * DP);
   Share *shares = reinterpret_cast<Share *>(part_ml + (size_t)kMaxRanges * 2 * C::kR);
-  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, part_o, part_ml,
-                                 shares))
+  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, kmap,
+                                 vmap, head_first, part_o, part_ml, shares))
     return e;
-  return launch_pdl(k_paged_merge<DP, T>, dim3(grid, C::kR / 8), dim3(256), 0, s, a, C::kR, part_o, part_ml, shares);
+  return launch_pdl(k_paged_merge<DP, T>, dim3(grid, NT), dim3(256), 0, s, a, C::kR, part_o, part_ml, shares);
+}
+
+// Tensor maps (head dim, then slot and head by stride, page) with boxes of 128
+// bytes x kb slots.  false, and the kernel loads key by key with cp.async,
+// where a block of kb keys could cross a page or the strides do not nest (each
+// a multiple of the one below and past its extent, as a tensor map wants).
+bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap, int *head_first) {
+  if (p.page_size % kb) return false;
+  const bool f32 = p.dtype == DCU_F32;
+  const uint64_t es = f32 ? 4 : 2, row = (uint64_t)p.head_dim * es;
+  uint64_t slot = (uint64_t)p.slot_stride * es, head = (uint64_t)p.head_stride * es;
+  if (p.n_kv_heads == 1) head = slot;  // the stride of a single head does not matter
+  const bool hf = head <= slot;
+  const uint64_t s0 = hf ? head : slot, s1 = hf ? slot : head;
+  const uint64_t n0 = hf ? (uint64_t)p.n_kv_heads : (uint64_t)p.page_size;
+  const uint64_t n1 = hf ? (uint64_t)p.page_size : (uint64_t)p.n_kv_heads;
+  const uint64_t s2 = p.n_pages == 1 ? s1 * n1 : (uint64_t)p.page_stride * es;
+  if (s0 < row || s1 < s0 * n0 || s1 % s0 || s2 < s1 * n1 || s2 % s1 || s2 >= (1ull << 40)) return false;
+  const uint64_t dims[4] = {(uint64_t)p.head_dim, n0, n1, (uint64_t)p.n_pages};
+  const uint64_t st[3] = {s0, s1, s2};
+  const uint32_t box[4] = {(uint32_t)(128 / es), hf ? 1u : (uint32_t)kb, hf ? (uint32_t)kb : 1u, 1u};
+  *head_first = hf;
+  return encode_tmap_4d(kmap, f32, p.k, dims, st, box) && encode_tmap_4d(vmap, f32, p.v, dims, st, box);
+}
+
+template <int DP, bool F32, int NT>
+cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  CUtensorMap kmap = {}, vmap = {};
+  int head_first = 0;
+  if (page_maps(a.pages, Cfg<DP, F32, NT>::kKB, &kmap, &vmap, &head_first))
+    return launch_variant<DP, F32, NT, true>(a, kmap, vmap, head_first, ws, s);
+  return launch_variant<DP, F32, NT, false>(a, kmap, vmap, head_first, ws, s);
+}
+
+// Tile width: one group of 8 queries when a sequence has at most 8 per kv head
+// on average (single tokens), else the widest tile.
+bool narrow(const PagedAttnArgs &a) {
+  return (long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B;
 }
 
 }  // namespace
 
 int64_t paged_attention_workspace(const dcu_pages &p) {
-  const bool f = p.dtype == DCU_F32;
-  if (p.head_dim <= 64) return f ? ws_bytes<64, true>() : ws_bytes<64, false>();
-  if (p.head_dim <= 128) return f ? ws_bytes<128, true>() : ws_bytes<128, false>();
-  return f ? ws_bytes<256, true>() : ws_bytes<256, false>();
+  if (p.dtype == DCU_F32)
+    return p.head_dim <= 64 ? ws_bytes<64, 1>() : p.head_dim <= 128 ? ws_bytes<128, 1>() : ws_bytes<256, 1>();
+  return p.head_dim <= 64 ? ws_bytes<64, 4>() : p.head_dim <= 128 ? ws_bytes<128, 4>() : ws_bytes<256, 2>();
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
-  const bool f = a.pages.dtype == DCU_F32;
-  if (a.pages.head_dim <= 64) return f ? launch<64, true>(a, ws, s) : launch<64, false>(a, ws, s);
-  if (a.pages.head_dim <= 128) return f ? launch<128, true>(a, ws, s) : launch<128, false>(a, ws, s);
-  return f ? launch<256, true>(a, ws, s) : launch<256, false>(a, ws, s);
+  const int hd = a.pages.head_dim;
+  if (a.pages.dtype == DCU_F32)
+    return hd <= 64 ? launch<64, true, 1>(a, ws, s)
+                    : hd <= 128 ? launch<128, true, 1>(a, ws, s) : launch<256, true, 1>(a, ws, s);
+  if (narrow(a))
+    return hd <= 64 ? launch<64, false, 1>(a, ws, s)
+                    : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
+  return hd <= 64 ? launch<64, false, 4>(a, ws, s)
+                  : hd <= 128 ? launch<128, false, 4>(a, ws, s) : launch<256, false, 2>(a, ws, s);
 }
 
 }  // namespace dcu

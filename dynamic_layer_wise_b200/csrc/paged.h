@@ -29,7 +29,8 @@ struct PagedAttnArgs {
   const int32_t *row_start, *kv_len, *table;
   dcu_pages pages;
   int32_t B, max_rows, max_pages, n_heads;
-  float scale_log2;  // scale * log2(e)
+  int32_t page_shift;  // log2(page_size), -1 when it is no power of two
+  float scale_log2;    // scale * log2(e)
   int32_t *status;
 };
 int64_t paged_attention_workspace(const dcu_pages &pages);
