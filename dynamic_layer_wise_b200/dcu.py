@@ -388,90 +388,93 @@ def dcu_set_apd(ctx: Context, alpha: float, beta: float, tau0: float = 0.9):
 # on; the caller keeps the inputs alive until that stream has passed the call.
 
 _DTYPE_CODE = {torch.bfloat16: DCU_BF16, torch.float32: DCU_F32}
+_I32 = torch.int32
 
 
-class _on:
-    """Makes `device` and `stream` (None: the device's current stream) current for the block; .raw is the stream."""
-
-    def __init__(self, device, stream):
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
-                torch.cuda.default_stream(device)
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors of {device}")
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
-        else:
-            self.ctx = None
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        self.raw = _vp((self.stream or torch.cuda.current_stream(self.device)).cuda_stream)
-        return self
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+# handle of a device's current stream without the Stream object around it (3 us of a call)
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _tensor(t, name: str, dtype, shape, device=None):
-    """Address of a contiguous CUDA tensor of `dtype` (None: any) and `shape` (None entries: any size) on `device`."""
+def _run(device, stream, call):
+    """call(raw stream) with `device` and `stream` (None: the device's current stream) current."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return call(_current_raw(device.index))
+        with torch.cuda.device(device):
+            return call(_current_raw(device.index))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError(f"stream of {stream.device} for tensors of {device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _arg(t, name: str, dtype, shape, device):
+    """Address of a contiguous CUDA tensor of `dtype`, `shape` and `device`."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: expected a tensor on {device or 'a CUDA device'}, got {t.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if len(shape) != t.dim() or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                     f"{device if device.type == 'cuda' else 'a CUDA device'}, got {t.dtype} {tuple(t.shape)} with "
+                     f"strides {t.stride()} on {t.device}")
+
+
+def _opt(t, name: str, dtype, shape, device):
+    return None if t is None else _arg(t, name, dtype, shape, device)
+
+
+def _dims(t, name: str, n: int):
+    """Shape of a tensor argument with n dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
 
 
 def _pages(k_pages, v_pages, device) -> dcu_pages:
     """dcu_pages of K and V tensors [n_pages][page_size][n_kv_heads][head_dim] (any strides but the last)."""
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if t.device != device:
-            raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-        if t.dim() != 4 or 0 in t.shape or (t.stride(3) != 1 and t.shape[3] != 1):
-            raise ValueError(f"{name}: expected [n_pages][page_size][n_kv_heads][head_dim] with a contiguous last "
-                             f"dimension, got {tuple(t.shape)} with strides {t.stride()}")
-    if k_pages.dtype not in _DTYPE_CODE or v_pages.dtype != k_pages.dtype:
-        raise ValueError("k_pages and v_pages must both be bfloat16 or both float32")
-    n, p, h, d = k_pages.shape
-    sn, sp, sh = (0 if m == 1 else s for m, s in zip(k_pages.shape, k_pages.stride()[:3]))
-    if v_pages.shape != k_pages.shape or any(m > 1 and s != t for m, s, t in zip(k_pages.shape, k_pages.stride(),
-                                                                                 v_pages.stride())):
-        raise ValueError("k_pages and v_pages must have the same shape and strides")
-    return dcu_pages(k_pages.data_ptr(), v_pages.data_ptr(), sn, sp, sh, n, p, h, d, _DTYPE_CODE[k_pages.dtype])
+    n, p, h, d = shape = _dims(k_pages, "k_pages", 4)
+    if _dims(v_pages, "v_pages", 4) != shape or v_pages.dtype != k_pages.dtype or k_pages.dtype not in _DTYPE_CODE:
+        raise ValueError("k_pages and v_pages must have one shape and both be bfloat16 or both float32")
+    if k_pages.device != device or v_pages.device != device:
+        raise ValueError(f"k_pages and v_pages: expected tensors on {device}, got {k_pages.device}, {v_pages.device}")
+    sn, sp, sh, sd = strides = k_pages.stride()
+    if v_pages.stride() != strides and any(m > 1 and a != b for m, a, b in zip(shape, strides, v_pages.stride())):
+        raise ValueError("k_pages and v_pages must have the same strides")
+    if (sd != 1 and d != 1) or 0 in shape:
+        raise ValueError(f"k_pages: expected [n_pages][page_size][n_kv_heads][head_dim] with a contiguous last "
+                         f"dimension, got {tuple(shape)} with strides {strides}")
+    return dcu_pages(k_pages.data_ptr(), v_pages.data_ptr(), sn if n > 1 else 0, sp if p > 1 else 0,
+                     sh if h > 1 else 0, n, p, h, d, _DTYPE_CODE[k_pages.dtype])
 
 
 def dcu_page_table(lens, page_size: int, max_pages: int, n_pages: int, pool=None, first=None, status=None,
                    stream=None):
     """Block table of B requests from their lengths (int32 [B]) over the free pages `pool` (int32; None: page i is
     entry i), beginning at entry `first` (int32 [1]; None: 0).  Returns (table [B][max_pages], held [B], next [1])."""
-    p_lens = _tensor(lens, "lens", torch.int32, (None,))
-    dev, B = lens.device, lens.shape[0]
-    p_pool = None if pool is None else _tensor(pool, "pool", torch.int32, (None,), dev)
-    p_first = None if first is None else _tensor(first, "first", torch.int32, (1,), dev)
-    p_status = None if status is None else _tensor(status, "status", torch.int32, (1,), dev)
+    B, = _dims(lens, "lens", 1)
+    dev = lens.device
+    n_pool = n_pages if pool is None else _dims(pool, "pool", 1)[0]
+    args = (_arg(lens, "lens", _I32, (B,), dev), B, page_size, max_pages, n_pages,
+            _opt(pool, "pool", _I32, (n_pool,), dev), n_pool, _opt(first, "first", _I32, (1,), dev))
+    p_status = _opt(status, "status", _I32, (1,), dev)
     if max_pages <= 0:
         raise ValueError("max_pages must be positive")
-    with _on(dev, stream) as on:
-        table = torch.empty((B, max_pages), dtype=torch.int32, device=dev)
-        held = torch.empty((B,), dtype=torch.int32, device=dev)
-        nxt = torch.empty((1,), dtype=torch.int32, device=dev)
-        _check(lib().dcu_page_table(p_lens, B, int(page_size), int(max_pages), int(n_pages), p_pool,
-                                    int(n_pages) if pool is None else pool.shape[0], p_first, table.data_ptr(),
-                                    held.data_ptr(), nxt.data_ptr(), p_status, on.raw))
-    return table, held, nxt
+
+    def call(raw):
+        table = torch.empty(B, max_pages, dtype=_I32, device=dev)
+        held = torch.empty(B, dtype=_I32, device=dev)
+        nxt = torch.empty(1, dtype=_I32, device=dev)
+        _check(lib().dcu_page_table(*args, table.data_ptr(), held.data_ptr(), nxt.data_ptr(), p_status, raw))
+        return table, held, nxt
+
+    return _run(dev, stream, call)
 
 
 def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=None, first=None, status=None,
@@ -479,35 +482,42 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
     """Packed rows of B sequences (count int32 [B]) at positions pos (int32 [B][N], e.g. idx of dcu_select_tokens)
     or first[b], first[b] + 1, ... (int32 [B]; None: from 0).  Returns (row_start [B + 1], row_pos, slot [max_rows]);
     entries at and after row_start[B] are not written."""
-    p_table = _tensor(table, "table", torch.int32, (None, None))
-    dev, B = table.device, table.shape[0]
-    p_count = _tensor(count, "count", torch.int32, (B,), dev)
-    p_pos = None if pos is None else _tensor(pos, "pos", torch.int32, (B, None), dev)
-    p_first = None if first is None else _tensor(first, "first", torch.int32, (B,), dev)
-    p_status = None if status is None else _tensor(status, "status", torch.int32, (1,), dev)
+    B, max_pages = _dims(table, "table", 2)
+    dev = table.device
+    N = 0 if pos is None else _dims(pos, "pos", 2)[1]
+    args = (_arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
+            _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
+            _opt(first, "first", _I32, (B,), dev), max_rows)
+    p_status = _opt(status, "status", _I32, (1,), dev)
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
-    with _on(dev, stream) as on:
-        row_start = torch.empty((B + 1,), dtype=torch.int32, device=dev)
-        row_pos = torch.empty((max_rows,), dtype=torch.int32, device=dev)
-        slot = torch.empty((max_rows,), dtype=torch.int32, device=dev)
-        _check(lib().dcu_slot_map(p_table, B, table.shape[1], int(page_size), int(n_pages), p_count, p_pos,
-                                  0 if pos is None else pos.shape[1], p_first, int(max_rows), row_start.data_ptr(),
-                                  row_pos.data_ptr(), slot.data_ptr(), p_status, on.raw))
-    return row_start, row_pos, slot
+
+    def call(raw):
+        row_start = torch.empty(B + 1, dtype=_I32, device=dev)
+        row_pos = torch.empty(max_rows, dtype=_I32, device=dev)
+        slot = torch.empty(max_rows, dtype=_I32, device=dev)
+        _check(lib().dcu_slot_map(*args, row_start.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), p_status, raw))
+        return row_start, row_pos, slot
+
+    return _run(dev, stream, call)
 
 
 def dcu_rope_table(max_pos: int, head_dim: int, theta: float = 10000.0, device="cuda", stream=None):
     """(cos, sin) of pos * theta^(-2j / head_dim): float32 [max_pos][head_dim / 2][2]."""
-    dev = torch.device(device)
-    if dev.index is None:
-        dev = torch.device("cuda", torch.cuda.current_device())
     if max_pos <= 0 or head_dim <= 0 or head_dim % 2:
         raise ValueError("max_pos and head_dim must be positive, head_dim even")
-    with _on(dev, stream) as on:
-        tab = torch.empty((max_pos, head_dim // 2, 2), dtype=torch.float32, device=dev)
-        _check(lib().dcu_rope_table(tab.data_ptr(), int(max_pos), int(head_dim), float(theta), on.raw))
-    return tab
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError("expected a CUDA device")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+
+    def call(raw):
+        tab = torch.empty(max_pos, head_dim // 2, 2, dtype=torch.float32, device=dev)
+        _check(lib().dcu_rope_table(tab.data_ptr(), max_pos, head_dim, theta, raw))
+        return tab
+
+    return _run(dev, stream, call)
 
 
 def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_heads: int, q=None, status=None,
@@ -516,29 +526,30 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
     into the pages (k_pages, v_pages: [n_pages][page_size][n_kv_heads][head_dim], any strides but the last), the
     first row_start[-1] rows.  rope: of dcu_rope_table, None for no rotation.  Returns q [T][n_heads][head_dim]
     (the given tensor when q is not None)."""
-    p_qkv = _tensor(qkv, "qkv", torch.float32, (None, None))
-    dev, T = qkv.device, qkv.shape[0]
+    T, width = _dims(qkv, "qkv", 2)
+    dev = qkv.device
     pages = _pages(k_pages, v_pages, dev)
-    if qkv.shape[1] != (n_heads + 2 * pages.n_kv_heads) * pages.head_dim:
-        raise ValueError(f"qkv: expected {(n_heads + 2 * pages.n_kv_heads) * pages.head_dim} columns, "
-                         f"got {qkv.shape[1]}")
-    p_start = _tensor(row_start, "row_start", torch.int32, (None,), dev)
-    p_pos = _tensor(row_pos, "row_pos", torch.int32, (T,), dev)
-    p_slot = _tensor(slot, "slot", torch.int32, (T,), dev)
-    if row_start.shape[0] < 1:
+    hd = pages.head_dim
+    if width != (n_heads + 2 * pages.n_kv_heads) * hd:
+        raise ValueError(f"qkv: expected {(n_heads + 2 * pages.n_kv_heads) * hd} columns, got {width}")
+    n_start, = _dims(row_start, "row_start", 1)
+    if n_start < 1:
         raise ValueError("row_start: expected at least one entry")
-    p_rope = None if rope is None else _tensor(rope, "rope", torch.float32, (None, pages.head_dim // 2, 2), dev)
-    p_status = None if status is None else _tensor(status, "status", torch.int32, (1,), dev)
-    shape = (T, n_heads, pages.head_dim)
+    max_pos = 0 if rope is None else _dims(rope, "rope", 3)[0]
+    args = (_arg(qkv, "qkv", torch.float32, (T, width), dev), T,
+            _arg(row_start, "row_start", _I32, (n_start,), dev) + 4 * (n_start - 1),
+            _arg(row_pos, "row_pos", _I32, (T,), dev), _arg(slot, "slot", _I32, (T,), dev),
+            _opt(rope, "rope", torch.float32, (max_pos, hd // 2, 2), dev), max_pos, n_heads, pages)
+    p_status = _opt(status, "status", _I32, (1,), dev)
     if q is not None:
-        _tensor(q, "q", k_pages.dtype, shape, dev)
-    with _on(dev, stream) as on:
-        if q is None:
-            q = torch.empty(shape, dtype=k_pages.dtype, device=dev)
-        _check(lib().dcu_paged_write(p_qkv, T, p_start + 4 * (row_start.shape[0] - 1), p_pos, p_slot, p_rope,
-                                     0 if rope is None else rope.shape[0], int(n_heads), ctypes.byref(pages),
-                                     q.data_ptr(), p_status, on.raw))
-    return q
+        _arg(q, "q", k_pages.dtype, (T, n_heads, hd), dev)
+
+    def call(raw):
+        out = torch.empty(T, n_heads, hd, dtype=k_pages.dtype, device=dev) if q is None else q
+        _check(lib().dcu_paged_write(*args, out.data_ptr(), p_status, raw))
+        return out
+
+    return _run(dev, stream, call)
 
 
 def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: float | None = None, out=None,
@@ -548,40 +559,35 @@ def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: fl
     block table (int32 [B][max_pages]).  scale defaults to head_dim^-1/2.  Returns out [T][n_heads][head_dim]; rows
     at and after row_start[B] are not written.  workspace: uint8, dcu_paged_attention_workspace bytes (None: allocated
     for the call)."""
-    dev = q.device if isinstance(q, torch.Tensor) else None
+    T, H, hd = _dims(q, "q", 3)
+    dev = q.device
     pages = _pages(k_pages, v_pages, dev)
-    p_q = _tensor(q, "q", k_pages.dtype, (None, None, pages.head_dim), dev)
-    T, H = q.shape[0], q.shape[1]
-    p_table = _tensor(table, "table", torch.int32, (None, None), dev)
-    B = table.shape[0]
-    p_start = _tensor(row_start, "row_start", torch.int32, (B + 1,), dev)
-    p_len = _tensor(kv_len, "kv_len", torch.int32, (B,), dev)
-    p_status = None if status is None else _tensor(status, "status", torch.int32, (1,), dev)
+    B, max_pages = _dims(table, "table", 2)
+    p_q = _arg(q, "q", k_pages.dtype, (T, H, pages.head_dim), dev)
+    args = (p_q, T, _arg(row_start, "row_start", _I32, (B + 1,), dev), B, _arg(kv_len, "kv_len", _I32, (B,), dev),
+            _arg(table, "table", _I32, (B, max_pages), dev), max_pages, H, pages,
+            hd ** -0.5 if scale is None else scale)
+    p_status = _opt(status, "status", _I32, (1,), dev)
     if out is not None:
-        _tensor(out, "out", k_pages.dtype, q.shape, dev)
+        _arg(out, "out", q.dtype, (T, H, hd), dev)
     if workspace is not None:
-        _tensor(workspace, "workspace", torch.uint8, (None,), dev)
-    if scale is None:
-        scale = pages.head_dim ** -0.5
-    with _on(dev, stream) as on:
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
-            workspace = torch.empty(_workspace_bytes(pages), dtype=torch.uint8, device=dev)
-        _check(lib().dcu_paged_attention(p_q, T, p_start, B, p_len, p_table, table.shape[1], H, ctypes.byref(pages),
-                                         float(scale), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                         p_status, on.raw))
-    return out
+        _arg(workspace, "workspace", torch.uint8, (_dims(workspace, "workspace", 1)[0],), dev)
+
+    def call(raw):
+        o = torch.empty_like(q) if out is None else out
+        ws = torch.empty(_workspace_bytes(pages), dtype=torch.uint8, device=dev) if workspace is None else workspace
+        _check(lib().dcu_paged_attention(*args, o.data_ptr(), ws.data_ptr(), ws.numel(), p_status, raw))
+        return o
+
+    return _run(dev, stream, call)
 
 
 def _workspace_bytes(pages: dcu_pages) -> int:
     n = _i64(0)
-    _check(lib().dcu_paged_attention_workspace(ctypes.byref(pages), ctypes.byref(n)))
+    _check(lib().dcu_paged_attention_workspace(pages, n))
     return n.value
 
 
 def dcu_paged_attention_workspace(k_pages, v_pages) -> int:
     """Bytes of the workspace tensor of dcu_paged_attention over these pages, on their device."""
-    pages = _pages(k_pages, v_pages, k_pages.device)
-    with torch.cuda.device(k_pages.device):
-        return _workspace_bytes(pages)
+    return _workspace_bytes(_pages(k_pages, v_pages, k_pages.device))
