@@ -26,16 +26,11 @@
 // split into a high and a low bf16 part, two products instead of one: the
 // weights keep 16 bits at a cost that the memory-bound loop hides.  float32
 // blocks run on the CUDA cores in fp32.
-#include <type_traits>
-
-#include "gemm_tc.h"
-#include "paged.h"
+#include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
 namespace dcu {
 namespace {
-
-constexpr int kMaxRanges = 148;  // most CTAs (work ranges) of a launch
 
 // One kernel variant: head dims up to DP (shorter ones zero-padded in shared memory).
 template <int DP, bool F32, int NT>
@@ -56,16 +51,6 @@ struct Cfg {
   static constexpr int kThreads = 32 * kW;
   static constexpr int kND = F32 ? (DP > 128 ? DP / 128 : 1) : 0;  // float32: 4-dim chunks of O per lane and query
   static constexpr int kAcc = F32 ? 8 * kND : DP / 16;           // float4s of O per lane and query group
-};
-
-// A share of an item that a range boundary cuts: what the merge needs.
-struct Share {
-  int32_t last;   // last range that holds a share of the item begun in this range; -1: none is cut here
-  int32_t row0;   // first packed row of the sequence
-  int32_t q0;     // first query (pair index in the sequence and kv head) of the tile
-  int32_t nq;     // queries of the tile
-  int32_t kvh;
-  int32_t slot;   // the share of this range: 0 its first segment, 1 its last one
 };
 
 __device__ __forceinline__ uint32_t su32(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -113,60 +98,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// key / page_size: a shift for the usual powers of two
-__device__ __forceinline__ unsigned div_page(const PagedAttnArgs &a, unsigned key) {
-  return a.page_shift >= 0 ? key >> a.page_shift : key / (unsigned)a.pages.page_size;
-}
-
-// The items of sequence b.
-struct Seq {
-  int row0, nq, tiles, tq, nk, nblk;  // first row, queries per kv head, tiles, queries per tile, keys, blocks per item
-  __device__ __forceinline__ long long units(int KV) const { return (long long)KV * tiles * nblk; }
-};
-template <int R, int KB>
-__device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
-  Seq s;
-  const int lo = min(max(a.row_start[b], 0), a.max_rows), hi = min(max(a.row_start[b + 1], 0), a.max_rows);
-  const int rows = max(hi - lo, 0);
-  s.row0 = lo;
-  s.nq = rows * (a.n_heads / a.pages.n_kv_heads);
-  s.tiles = (s.nq + R - 1) / R;
-  s.tq = s.tiles ? ((s.nq + s.tiles - 1) / s.tiles + 7) / 8 * 8 : 0;
-  const long long cap = (long long)a.max_pages * a.pages.page_size;
-  const int n = max(a.kv_len[b], 0);
-  if (n > cap && rows && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
-  s.nk = (int)min((long long)n, cap);
-  s.nblk = max(1, (int)(((long long)s.nk + KB - 1) / KB));  // an empty sequence still gets its zeros
-  return s;
-}
-
-// A place in the line of units: block blk of (b, kv head, tile).
-struct Place {
-  int b, kvh, tile, blk;
-  Seq s;
-};
-template <int R, int KB>
-__device__ __forceinline__ void next_seq(const PagedAttnArgs &a, Place &p) {
-  while (++p.b < a.B) {
-    p.s = seq_of<R, KB>(a, p.b);
-    if (p.s.tiles) break;
-  }
-}
-template <int R, int KB>
-__device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n) {
-  p.blk += n;
-  while (p.b < a.B && p.blk >= p.s.nblk) {
-    p.blk -= p.s.nblk;
-    if (++p.tile == p.s.tiles) {
-      p.tile = 0;
-      if (++p.kvh == a.pages.n_kv_heads) {
-        p.kvh = 0;
-        next_seq<R, KB>(a, p);
-      }
-    }
-  }
-}
-
 // 16-byte chunk c of key row r in a block's K or V: boxes of KB rows x 128
 // bytes with the 128-byte swizzle (the layout that a TMA tile load writes).
 template <int KB>
@@ -200,7 +131,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
   constexpr uint32_t FULL = (1u << KB) - 1u;
   pdl_enter();
   extern __shared__ uint8_t sm_raw[];
-  __shared__ long long s_scan[32];
+  __shared__ long long s_scan[W];
   __shared__ Place s_place;
   __shared__ uint32_t s_mask[W][NST];
   __shared__ float2 s_ml[W][R];
@@ -216,53 +147,13 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
     s_abort = 0;
   }
 
-  // ---- this CTA's range [u0, u1) of the units and its first place
-  long long u0, u1, total;
-  int ranges;
-  {
-    const int per = (a.B + C::kThreads - 1) / C::kThreads;
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_of<R, KB>(a, b).units(KV);
-    long long x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_scan[warp] = x;
-    __syncthreads();
-    long long base = 0;
-    total = 0;
-    for (int i = 0; i < W; ++i) {
-      if (i == warp) base = total;
-      total += s_scan[i];
-    }
-    // at least one block per warp in a range
-    ranges = (int)min((long long)gridDim.x, (total + W - 1) / W);
-    if ((int)blockIdx.x >= ranges) {
-      if (tid == 0) shares[blockIdx.x].last = -1;
-      return;
-    }
-    u0 = total * blockIdx.x / ranges;
-    u1 = total * (blockIdx.x + 1) / ranges;
-    long long at = base + x - mine;
-    if (u0 >= at && u0 < at + mine) {  // exactly one thread
-      Place p;
-      for (p.b = b0; p.b < b1; ++p.b) {
-        p.s = seq_of<R, KB>(a, p.b);
-        if (u0 < at + p.s.units(KV)) break;
-        at += p.s.units(KV);
-      }
-      const long long off = u0 - at;
-      const long long item = off / p.s.nblk;
-      p.blk = (int)(off - item * p.s.nblk);
-      p.kvh = (int)(item / p.s.tiles);
-      p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
-      s_place = p;
-    }
-    __syncthreads();
+  // ---- this CTA's range of the units and its first place
+  const Range rg = find_range<R, KB, W>(a, &s_place, s_scan);
+  if (!rg.any) {
+    if (tid == 0) shares[blockIdx.x].last = -1;
+    return;
   }
+  const long long u0 = rg.u0, u1 = rg.u1;
   Place seg = s_place;  // start of the current segment (the part of an item inside the range)
 
   uint8_t *sm = sm_raw + ((1024u - (su32(sm_raw) & 1023u)) & 1023u);
@@ -751,9 +642,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
       Share sh;
       sh.last = -1;
       if (starts && !ends) {
-        // the range that holds the item's last unit
-        const long long last_u = s0 + sq.nblk - 1;
-        sh.last = (int)(((last_u + 1) * ranges + total - 1) / total) - 1;
+        sh.last = rg.of(s0 + sq.nblk - 1);
         sh.row0 = sq.row0;
         sh.q0 = q0;
         sh.nq = nq;
@@ -823,31 +712,31 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Workspace: shares' O, (max, sum), descriptors; two shares per range at most.
-template <int DP, int NT>
-constexpr int64_t ws_bytes() {
-  return (int64_t)kMaxRanges * 2 * 8 * NT * (DP * 4 + 8) + (int64_t)kMaxRanges * sizeof(Share);
-}
-
 template <int DP, bool F32, int NT, bool TMA>
 cudaError_t launch_variant(const PagedAttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int head_first,
                            void *ws, cudaStream_t s) {
   using C = Cfg<DP, F32, NT>;
-  using T = std::conditional_t<F32, float, bf16>;
   static std::atomic<uint64_t> attr{0};
   if (cudaError_t e = ensure_smem_limit(k_paged_attn<DP, F32, NT, TMA>, C::kSmem, attr)) return e;
-  int dev = 0, sms = 0;
-  if (cudaError_t e = cudaGetDevice(&dev)) return e;
-  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
-  const int grid = sms < kMaxRanges ? sms : kMaxRanges;
-  float *part_o = static_cast<float *>(ws);
-  float2 *part_ml = reinterpret_cast<float2 *>(part_o + (size_t)kMaxRanges * 2 * C::kR * DP);
-  Share *shares = reinterpret_cast<Share *>(part_ml + (size_t)kMaxRanges * 2 * C::kR);
+  int grid = 0;
+  if (cudaError_t e = paged_grid(&grid)) return e;
+  const ShareBuf sb(ws, C::kR, DP);
   if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, kmap,
-                                 vmap, head_first, part_o, part_ml, shares))
+                                 vmap, head_first, sb.o, sb.ml, sb.desc))
     return e;
-  return launch_pdl(k_paged_merge<DP, T>, dim3(grid, NT), dim3(256), 0, s, a, C::kR, part_o, part_ml, shares);
+  return launch_paged_merge(a, C::kR, grid, sb, s);
 }
+
+template <int DP, bool F32, int NT>
+cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  CUtensorMap kmap = {}, vmap = {};
+  int head_first = 0;
+  if (page_maps(a.pages, Cfg<DP, F32, NT>::kKB, &kmap, &vmap, &head_first))
+    return launch_variant<DP, F32, NT, true>(a, kmap, vmap, head_first, ws, s);
+  return launch_variant<DP, F32, NT, false>(a, kmap, vmap, head_first, ws, s);
+}
+
+}  // namespace
 
 // Tensor maps (head dim, then slot and head by stride, page) with boxes of 128
 // bytes x kb slots.  false, and the kernel loads key by key with cp.async,
@@ -872,27 +761,29 @@ bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap,
   return encode_tmap_4d(kmap, f32, p.k, dims, st, box) && encode_tmap_4d(vmap, f32, p.v, dims, st, box);
 }
 
-template <int DP, bool F32, int NT>
-cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
-  CUtensorMap kmap = {}, vmap = {};
-  int head_first = 0;
-  if (page_maps(a.pages, Cfg<DP, F32, NT>::kKB, &kmap, &vmap, &head_first))
-    return launch_variant<DP, F32, NT, true>(a, kmap, vmap, head_first, ws, s);
-  return launch_variant<DP, F32, NT, false>(a, kmap, vmap, head_first, ws, s);
+cudaError_t paged_grid(int *grid) {
+  int dev = 0, sms = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  if (cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) return e;
+  *grid = sms < kMaxRanges ? sms : kMaxRanges;
+  return cudaSuccess;
 }
 
-// Tile width: one group of 8 queries when a sequence has at most 8 per kv head
-// on average (single tokens), else the widest tile.
-bool narrow(const PagedAttnArgs &a) {
-  return (long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B;
+cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s) {
+  const int hd = a.pages.head_dim;
+  const dim3 g(grid, kr / 8 < 4 ? kr / 8 : 4);
+  auto go = [&](auto kern) { return launch_pdl(kern, g, dim3(256), 0, s, a, kr, sb.o, sb.ml, sb.desc); };
+  if (a.pages.dtype == DCU_F32)
+    return hd <= 64 ? go(k_paged_merge<64, float>) : hd <= 128 ? go(k_paged_merge<128, float>)
+                                                               : go(k_paged_merge<256, float>);
+  return hd <= 64 ? go(k_paged_merge<64, bf16>) : hd <= 128 ? go(k_paged_merge<128, bf16>)
+                                                            : go(k_paged_merge<256, bf16>);
 }
-
-}  // namespace
 
 int64_t paged_attention_workspace(const dcu_pages &p) {
-  if (p.dtype == DCU_F32)
-    return p.head_dim <= 64 ? ws_bytes<64, 1>() : p.head_dim <= 128 ? ws_bytes<128, 1>() : ws_bytes<256, 1>();
-  return p.head_dim <= 64 ? ws_bytes<64, 4>() : p.head_dim <= 128 ? ws_bytes<128, 4>() : ws_bytes<256, 2>();
+  const int dp = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
+  if (p.dtype == DCU_F32) return ShareBuf::bytes(8, dp);
+  return dp == 256 ? ShareBuf::bytes(16, dp) : ShareBuf::bytes(kTcQueries, dp);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
@@ -900,9 +791,12 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
   if (a.pages.dtype == DCU_F32)
     return hd <= 64 ? launch<64, true, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, true, 1>(a, ws, s) : launch<256, true, 1>(a, ws, s);
-  if (narrow(a))
+  // queries per sequence and kv head, on average (max_rows bounds the rows)
+  const long long queries = (long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads);
+  if (queries <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
+  if (queries > 32ll * a.B && a.scale_log2 > 0.f && tc_box_keys(a.pages)) return launch_paged_attention_tc(a, ws, s);
   return hd <= 64 ? launch<64, false, 4>(a, ws, s)
                   : hd <= 128 ? launch<128, false, 4>(a, ws, s) : launch<256, false, 2>(a, ws, s);
 }

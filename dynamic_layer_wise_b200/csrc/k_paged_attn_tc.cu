@@ -1,0 +1,474 @@
+// Paged attention of many query rows per sequence on the 5th-gen tensor cores
+// (bf16, head_dim up to 128).  Same line of work, shares and merge as
+// k_paged_attn.cu, with items of up to 256 queries (two MMA tiles of 128, one
+// TMEM lane per query) and units of 128 keys:
+//
+//   warp 0     TMA producer: the pages of a chunk of 128 keys, boxes of
+//              box_keys slots x 64 dims (128-byte swizzle), K and V rings of
+//              two stages; a box past the sequence's end or on a bad page is
+//              read at a page coordinate outside the tensor, i.e. as zeros
+//   warp 1     MMA issuer (one thread): S_t = Q_t K^T (M = 128 queries, N = 128
+//              keys) and O_t += P_t V (P_t in tensor memory, V MN-major), for
+//              the tiles t = A, B in turn
+//   warps 2-9 and 10-17  softmax of tile A and of tile B: thread = (query, half
+//              of the chunk's keys)
+//
+// The two tiles share every K and V stage and keep the two engines busy in
+// turn: while the softmax of one tile runs, the tensor core works for the other.
+// TMEM: S_A, S_B, O_A, O_B of 128 columns each; each half's P_t (bf16 pairs)
+// overwrites scores that its threads have read, and S_t of the next chunk waits
+// for P_t V.
+// P is rounded to bf16 once, as in the dense attention of a step: a second
+// product for the low part would cost half as much again on the pipe that
+// bounds this kernel.
+//
+// Every mbarrier wait is bounded; on expiry the CTA sets DCU_ST_TIMEOUT, drains
+// its copies and MMAs in flight, frees TMEM and exits.
+#include "paged_attn.cuh"
+#include "tc_ptx.cuh"
+
+namespace dcu {
+namespace {
+
+constexpr int kKC = 128;              // keys of a unit
+constexpr int kStages = 2;            // K and V ring depth
+constexpr int kSoftWarps = 8;         // per tile
+constexpr int kWarps = 2 + 2 * kSoftWarps;
+constexpr int kThreads = 32 * kWarps;
+
+template <int DP>
+struct TcCfg {
+  static constexpr uint32_t kTile = 128u * DP * 2u;  // a Q tile, or K or V of a chunk: DP / 64 blocks of 16 KB
+  static constexpr uint32_t kSmem = (2 + 2 * kStages) * kTile + 1024u;
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kO = 256;                // O_t at column 256 + 128 t
+};
+
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {  // 16-byte chunk c of row r
+  return (uint32_t)(c >> 3) * 16384u + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+}
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2a(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t packb(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// Valid keys of a half chunk as two words: the first nv keys, less the boxes in `bad`.
+__device__ __forceinline__ uint2 valid_keys(int nv, uint32_t bad, int box) {
+  unsigned long long m = nv >= 64 ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if ((bad >> i) & 1u) m &= ~((box >= 64 ? ~0ull : (1ull << box) - 1ull) << (i * box & 63));
+  return make_uint2((uint32_t)m, (uint32_t)(m >> 32));
+}
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], uint32_t valid) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!((valid >> c) & 1u)) r[c] = 0xff800000u;  // -inf
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_paged_attn_tc(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap, int head_first, int box, float *__restrict__ part_o,
+                    float2 *__restrict__ part_ml, Share *__restrict__ shares) {
+  using C = TcCfg<DP>;
+  constexpr int R = kTcQueries, OC = DP / 2;  // O columns of a half
+  extern __shared__ uint8_t sm_raw[];
+  __shared__ __align__(8) uint64_t bars[4 * kStages + 9];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ long long s_scan[kWarps];
+  __shared__ Place s_place;
+  __shared__ float s_mx[2][2][2][128];  // [chunk parity][tile][half] maximum of the half's keys
+  __shared__ float s_l[2][2][128];      // [tile][half] share of the row sum
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
+  uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
+  const uint32_t q_s = sbase, k_s = sbase + 2 * C::kTile, v_s = k_s + kStages * C::kTile;
+  const uint32_t bar0 = smem_u32(bars);
+  auto K_FULL = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto K_EMPTY = [&](uint32_t s) { return bar0 + 8u * (kStages + s); };
+  auto V_FULL = [&](uint32_t s) { return bar0 + 8u * (2 * kStages + s); };
+  auto V_EMPTY = [&](uint32_t s) { return bar0 + 8u * (3 * kStages + s); };
+  auto S_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + t); };
+  auto P_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + 2 + t); };
+  auto PV_DONE = [&](int t) { return bar0 + 8u * (4 * kStages + 4 + t); };
+  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 6), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;
+
+  if (tid == 0) {
+    for (int s = 0; s < 4 * kStages; ++s) mbar_init(bar0 + 8u * s, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(S_FULL(t), 1);
+      mbar_init(P_FULL(t), kSoftWarps);
+      mbar_init(PV_DONE(t), 1);
+    }
+    mbar_init(Q_FULL, 2 * kSoftWarps);
+    mbar_init(O_FINAL, 1);
+    mbar_init(DRAIN, 1);
+    abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  pdl_enter();
+  fence_proxy_async_global();  // the pages may have been written by the kernel just waited for
+  tc_fence_before();
+  const Range rg = find_range<R, kKC, kWarps>(a, &s_place, s_scan, 1);  // (barriers inside)
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  volatile int *abort_v = &abort_flag;
+  const int KV = a.pages.n_kv_heads, G = a.n_heads / KV, hd = a.pages.head_dim;
+
+  if (!rg.any) {
+    if (tid == 0) shares[blockIdx.x].last = -1;
+  } else if (warp == 0) {
+    // ---- TMA producer
+    Place ld = s_place;
+    const int nb = kKC / box;                     // boxes of a chunk (of each 64-dim half)
+    const int my = lane % nb, half = lane / nb;   // the lane's box: lanes 0 .. nb * DP / 64 - 1 issue
+    const bool mine = half < DP / 64;
+    auto look = [&]() {
+      const int key = ld.blk * kKC + my * box;
+      return mine && key < ld.s.nk ? a.table[(size_t)ld.b * a.max_pages + div_page(a, (unsigned)key)] : -1;
+    };
+    int pg = look();
+    uint32_t issued = 0;
+    bool ok = true;
+    for (long long u = rg.u0; u < rg.u1 && ok; ++u) {
+      const uint32_t st = issued % kStages, ph = ((issued / kStages) & 1u) ^ 1u;
+      const int key = ld.blk * kKC + my * box, kvh = ld.kvh;
+      const bool in = mine && key < ld.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
+      if (in && !good && half == 0 && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+      const int w = good ? pg : a.pages.n_pages;  // outside the tensor: zeros
+      const int y = good ? key - (int)(div_page(a, (unsigned)key) * (unsigned)a.pages.page_size) : 0;
+      const int c1 = head_first ? kvh : y, c2 = head_first ? y : kvh;
+      const uint32_t dst = (uint32_t)half * 16384u + (uint32_t)(my * box) * 128u;
+      if (u + 1 < rg.u1) {
+        advance<R, kKC>(a, ld, 1);
+        pg = look();
+      }
+      for (int v = 0; v < 2 && ok; ++v) {
+        ok = __all_sync(0xffffffffu, wait_bounded(v ? V_EMPTY(st) : K_EMPTY(st), ph, abort_v, a.status));
+        if (!ok) break;
+        const uint32_t bar = v ? V_FULL(st) : K_FULL(st);
+        if (lane == 0) mbar_expect_tx(bar, C::kTile);
+        __syncwarp();
+        if (mine) tma_box((v ? v_s : k_s) + st * C::kTile + dst, v ? &vmap : &kmap, half * 64, c1, c2, w, bar);
+        if (v) ++issued;
+      }
+    }
+    if (!ok) {  // wait, bounded, for the copies still in flight
+      for (uint32_t s = 0; s < kStages; ++s) {
+        const uint32_t nk = issued > s ? (issued - 1 - s) / kStages : 0;  // last full phase of the stage
+        if (issued > s) {
+          wait_drain(K_FULL(s), nk & 1u);
+          wait_drain(V_FULL(s), nk & 1u);
+        }
+      }
+      const uint32_t s = issued % kStages;  // a K load whose V was not issued (ends at once if there was none)
+      wait_drain(K_FULL(s), (issued / kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16(128, kKC), id_o = idesc_bf16_bmn(128, DP);
+      bool ok = true, any = false;
+      uint32_t g = 0, nseg = 0;          // chunks and segments done
+      uint32_t cnt[2] = {0, 0};          // chunks of each tile done
+      uint32_t pvs[2] = {0, 0};          // PV_DONE phases of each tile
+      auto wait = [&](uint32_t bar, uint32_t par) { return ok = ok && wait_bounded(bar, par & 1u, abort_v, a.status); };
+      auto issue_s = [&](int t, uint32_t st) {
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * 16384u;
+          tc_mma(tmem + 128u * t, sw128_desc(q_s + t * C::kTile + off) + (uint64_t)(2 * (kk & 3)),
+                 sw128_desc(k_s + st * C::kTile + off) + (uint64_t)(2 * (kk & 3)), id_s, kk > 0 ? 1u : 0u);
+        }
+        any = true;
+        tc_commit(S_FULL(t));
+      };
+      Place seg = s_place;
+      for (long long s0 = rg.u0; s0 < rg.u1 && ok;) {
+        const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
+        const int n = (int)(s1 - s0);
+        const int nt = min(seg.s.tq, seg.s.nq - seg.tile * seg.s.tq) > 128 ? 2 : 1;
+        if (!wait(Q_FULL, nseg) || !wait(K_FULL(g % kStages), g / kStages)) break;
+        tc_fence_after();
+        for (int t = 0; t < nt; ++t) issue_s(t, g % kStages);
+        tc_commit(K_EMPTY(g % kStages));
+        for (int j = 0; j < n && ok; ++j, ++g) {
+          const uint32_t st = g % kStages, st1 = (g + 1) % kStages;
+          for (int t = 0; t < nt && ok; ++t) {
+            if (!wait(P_FULL(t), cnt[t]) || (t == 0 && !wait(V_FULL(st), g / kStages))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kKC / 16; ++kk)
+              tc_mma_ts(tmem + C::kO + 128u * t, tmem + 128u * t + (uint32_t)((kk >> 2) * 64 + 32 + (kk & 3) * 8),
+                        sw128_mn_desc(v_s + st * C::kTile + (uint32_t)kk * 2048u, 16384u), id_o,
+                        (j > 0 || kk > 0) ? 1u : 0u);
+            if (t == nt - 1) tc_commit(V_EMPTY(st));
+            if (j + 1 < n) {
+              // S_t of the next chunk overwrites P_t: after P_t V has read it
+              tc_commit(PV_DONE(t));
+              if (!wait(PV_DONE(t), pvs[t]++) || (t == 0 && !wait(K_FULL(st1), (g + 1) / kStages))) break;
+              tc_fence_after();
+              issue_s(t, st1);
+              if (t == nt - 1) tc_commit(K_EMPTY(st1));
+            }
+            ++cnt[t];
+          }
+        }
+        if (!ok) break;
+        tc_commit(O_FINAL);
+        ++nseg;
+        advance<R, kKC>(a, seg, n);
+        s0 = s1;
+      }
+      if (!ok && any) {
+        tc_commit(DRAIN);
+        wait_drain(DRAIN, 0);
+      }
+    }
+  } else {
+    // ---- softmax
+    const int t = (warp - 2) / kSoftWarps, pt = ((warp - 2) % kSoftWarps) / 4, q4 = warp & 3;
+    const int qi = q4 * 32 + lane;                       // query of the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t s_tm = tmem + 128u * t + lane_off, o_tm = tmem + C::kO + 128u * t + lane_off + (uint32_t)(pt * OC);
+    const int st_id = tid - 64;
+    const float sc = a.scale_log2;
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q4) : "memory"); };
+    uint32_t cnt = 0, g = 0, nseg = 0;  // chunks of this tile, of the CTA, segments
+    bool alive = true;
+    const int nbh = 64 / box > 0 ? 64 / box : 1;  // boxes of a half (a box of 128 slots spans both)
+    Place seg = s_place;
+    for (long long s0 = rg.u0; s0 < rg.u1; ++nseg) {
+      const Seq &sq = seg.s;
+      const long long s1 = min(rg.u1, s0 + (sq.nblk - seg.blk));
+      const int n = (int)(s1 - s0);
+      const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
+      const bool on = t == 0 || nq > 128;
+      // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read
+      // theirs (O_FINAL)
+      {
+        const int rows = nq > 128 ? 256 : 128;
+        for (int i = st_id; i < rows * (DP / 8); i += 64 * kSoftWarps) {
+          const int r = i / (DP / 8), c = i - r * (DP / 8);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (r < nq && c * 8 < hd) {
+            const int pq = q0 + r, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+            v = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.q) + ((size_t)row * a.n_heads + h) * hd +
+                                                 c * 8);
+          }
+          *reinterpret_cast<uint4 *>(sm + (uint32_t)(r >> 7) * C::kTile + tile_off(r & 127, c)) = v;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(Q_FULL);
+      }
+      if (on) {
+        float m_run = -INFINITY, l_run = 0.f;
+        // the pages of this half's boxes, looked up a chunk ahead
+        auto look = [&](int blk) {
+          const int key = blk * kKC + pt * 64 + lane * box;
+          return lane < nbh && key < sq.nk ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)] : 0;
+        };
+        int pg = look(seg.blk);
+        for (int j = 0; j < n; ++j) {
+          const int key0 = (seg.blk + j) * kKC;
+          const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.pages.n_pages);
+          if (j + 1 < n) pg = look(seg.blk + j + 1);
+          if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(t), cnt & 1u, abort_v, a.status));
+          const int nv = sq.nk - key0 - pt * 64;  // valid keys of this half
+          // Raw scores: the scale (> 0) commutes with the maximum and enters the exponent.  The first 32 keys are read
+          // again for the exponentials rather than kept, which holds the thread within 96 registers.
+          const bool cut = nv < 64 || bad;
+          const uint2 valid = cut ? valid_keys(nv, bad, box) : make_uint2(~0u, ~0u);
+          uint32_t sr[32];
+          float mc = -INFINITY;
+          if (alive) {
+            tc_fence_after();
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              tmem_ld32_issue(s_tm + (uint32_t)(pt * 64 + hf * 32), sr);
+              tmem_wait_ld_tie32(sr);
+              if (cut) mask32(sr, hf ? valid.y : valid.x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
+            }
+            mc = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
+          s_mx[cnt & 1][t][pt][qi] = mc;
+          pair_sync();
+          mc = fmaxf(mc, s_mx[cnt & 1][t][1 - pt][qi]);
+          ++cnt;
+          const uint32_t gj = g + (uint32_t)j;
+          if (!alive) continue;
+          // The maximum moves only when a chunk exceeds it by more than 8 (log2 units): P stays below 2^8, most
+          // chunks rescale nothing, and P, the sum and O share it.
+          const bool grow = mc > m_run + 8.f;
+          const float m_new = grow ? mc : m_run;
+          const float alpha = grow ? (m_run == -INFINITY ? 0.f : ex2a(m_run - m_new)) : 1.f;
+          if (j > 0 && __any_sync(0xffffffffu, grow)) {  // P V of the last chunk is complete: S_FULL follows it
+#pragma unroll 1
+            for (int c = 0; c < OC / 16; ++c) {
+              float ov[16];
+              tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+              tmem_st16(o_tm + (uint32_t)(c * 16), ov);
+            }
+          }
+          m_run = m_new;
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          // P of this half goes over its own scores of keys 32 .. 63, which are in registers by then: columns 64 pt + 32 .. + 64
+          // (16 per 32 keys)
+#pragma unroll
+          for (int hf = 1; hf >= 0; --hf) {
+            if (hf == 0) {
+              tmem_ld32_issue(s_tm + (uint32_t)(pt * 64), sr);
+              tmem_wait_ld_tie32(sr);
+              if (cut) mask32(sr, valid.x);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float p0 = ex2a(fmaf(__uint_as_float(sr[2 * c]), sc, -m_use));
+              const float p1 = ex2a(fmaf(__uint_as_float(sr[2 * c + 1]), sc, -m_use));
+              ps[c & 3] += p0 + p1;
+              pk[c] = packb(p0, p1);
+            }
+            tmem_st16u(s_tm + (uint32_t)(pt * 64 + (hf ? 48 : 32)), pk);
+          }
+          l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+          if (t == 0 && sq.nk - key0 < kKC) {
+            // past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
+            // zeros; the rows are cleared after the copy and before P_FULL lets P V start.
+            alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(gj % kStages), (gj / kStages) & 1u, abort_v, a.status));
+            if (!alive) continue;
+            const int r0 = max(sq.nk - key0, 0), r1 = min(kKC, (r0 + box - 1) / box * box);
+            for (int i = st_id; i < (r1 - r0) * (DP / 8); i += 32 * kSoftWarps)
+              *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kStages) * C::kTile +
+                                         tile_off(r0 + i / (DP / 8), i % (DP / 8))) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(P_FULL(t));
+        }
+        // ---- the segment's end
+        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
+        s_l[t][pt][qi] = l_run;
+        pair_sync();
+        const float l = s_l[t][0][qi] + s_l[t][1][qi];
+        const bool starts = seg.blk == 0, ends = n == sq.nblk - seg.blk;
+        const int slot = s0 == rg.u0 ? 0 : 1, q = t * 128 + qi;
+        if (alive) {
+          tc_fence_after();
+          const int pq = q0 + q, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+          bf16 *dst = static_cast<bf16 *>(a.out) + ((size_t)row * a.n_heads + h) * hd + pt * OC;
+          const size_t share = ((size_t)blockIdx.x * 2 + slot) * R + q;
+          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+          for (int c = 0; c < OC / 16; ++c) {
+            float ov[16];
+            tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
+            if (q < nq && pt * OC + c * 16 < hd) {
+              if (starts && ends) {
+                uint4 *d = reinterpret_cast<uint4 *>(dst + c * 16);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  d[e] = make_uint4(packb(ov[8 * e] * inv, ov[8 * e + 1] * inv),
+                                    packb(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv),
+                                    packb(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv),
+                                    packb(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv));
+              } else {
+                float4 *d = reinterpret_cast<float4 *>(part_o + share * DP + pt * OC + c * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  d[e] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+              }
+            }
+          }
+          if (q < nq && pt == 0 && !(starts && ends)) part_ml[share] = make_float2(m_run, l);
+          tc_fence_before();
+        }
+        if (s1 == rg.u1 && st_id == 0) {
+          Share sh;
+          sh.last = starts && !ends && alive ? rg.of(s0 + sq.nblk - 1) : -1;
+          sh.row0 = sq.row0;
+          sh.q0 = q0;
+          sh.nq = nq;
+          sh.kvh = seg.kvh;
+          sh.slot = slot;
+          shares[blockIdx.x] = sh;
+        }
+      } else {
+        // tile B sits this segment out; its queries' buffer is not rewritten before the segment's MMAs are done
+        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
+      }
+      g += (uint32_t)n;
+      advance<R, kKC>(a, seg, n);
+      s0 = s1;
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int DP>
+cudaError_t launch_dp(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  using C = TcCfg<DP>;
+  static std::atomic<uint64_t> attr{0};
+  if (cudaError_t e = ensure_smem_limit(k_paged_attn_tc<DP>, (int)C::kSmem, attr)) return e;
+  CUtensorMap kmap, vmap;
+  int head_first = 0, grid = 0;
+  const int box = tc_box_keys(a.pages);
+  if (!box || !page_maps(a.pages, box, &kmap, &vmap, &head_first)) return cudaErrorInvalidValue;
+  if (cudaError_t e = paged_grid(&grid)) return e;
+  const ShareBuf sb(ws, kTcQueries, DP);
+  if (cudaError_t e = launch_pdl(k_paged_attn_tc<DP>, dim3(grid), dim3(kThreads), C::kSmem, s, a, kmap, vmap,
+                                 head_first, box, sb.o, sb.ml, sb.desc))
+    return e;
+  return launch_paged_merge(a, kTcQueries, grid, sb, s);
+}
+
+}  // namespace
+
+int tc_box_keys(const dcu_pages &p) {
+  CUtensorMap k, v;
+  int hf = 0;
+  if (p.dtype != DCU_BF16 || p.head_dim > 128) return 0;
+  int box = 16;
+  while (box < 128 && p.page_size % (2 * box) == 0) box *= 2;
+  return page_maps(p, box, &k, &v, &hf) ? box : 0;
+}
+
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+  return a.pages.head_dim <= 64 ? launch_dp<64>(a, ws, s) : launch_dp<128>(a, ws, s);
+}
+
+}  // namespace dcu

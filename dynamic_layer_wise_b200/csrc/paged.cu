@@ -22,6 +22,7 @@ int pg_fail(int code, const char *msg) noexcept {
 
 int pg_cuda(cudaError_t e, const char *call) noexcept {
   if (e == cudaSuccess) return DCU_OK;
+  cudaGetLastError();  // reported here: not left for the next call
   try {
     set_global_error((std::string(call) + ": " + cudaGetErrorString(e)).c_str());
   } catch (...) {

@@ -1,0 +1,164 @@
+// The line of work of the paged attention kernels: every (sequence, kv head,
+// query tile) is an item of ceil(keys / KB) units, units are numbered in item
+// order, and each CTA takes an equal range of them.  Lengths and rows are only
+// on the device, so each CTA derives the cut itself.
+#pragma once
+#include "common.cuh"
+#include "gemm_tc.h"
+#include "paged.h"
+
+namespace dcu {
+
+constexpr int kMaxRanges = 148;  // most CTAs (work ranges) of a launch
+
+// A share of an item that a range boundary cuts: what the merge needs.
+struct Share {
+  int32_t last;   // last range that holds a share of the item begun in this range; -1: none is cut here
+  int32_t row0;   // first packed row of the sequence
+  int32_t q0;     // first query (pair index in the sequence and kv head) of the tile
+  int32_t nq;     // queries of the tile
+  int32_t kvh;
+  int32_t slot;   // the share of this range: 0 its first segment, 1 its last one
+};
+
+namespace {
+
+// key / page_size: a shift for the usual powers of two
+__device__ __forceinline__ unsigned div_page(const PagedAttnArgs &a, unsigned key) {
+  return a.page_shift >= 0 ? key >> a.page_shift : key / (unsigned)a.pages.page_size;
+}
+
+// The items of sequence b.
+struct Seq {
+  int row0, nq, tiles, tq, nk, nblk;  // first row, queries per kv head, tiles, queries per tile, keys, blocks per item
+  __device__ __forceinline__ long long units(int KV) const { return (long long)KV * tiles * nblk; }
+};
+template <int R, int KB>
+__device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
+  Seq s;
+  const int lo = min(max(a.row_start[b], 0), a.max_rows), hi = min(max(a.row_start[b + 1], 0), a.max_rows);
+  const int rows = max(hi - lo, 0);
+  s.row0 = lo;
+  s.nq = rows * (a.n_heads / a.pages.n_kv_heads);
+  s.tiles = (s.nq + R - 1) / R;
+  s.tq = s.tiles ? ((s.nq + s.tiles - 1) / s.tiles + 7) / 8 * 8 : 0;
+  const long long cap = (long long)a.max_pages * a.pages.page_size;
+  const int n = max(a.kv_len[b], 0);
+  if (n > cap && rows && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+  s.nk = (int)min((long long)n, cap);
+  s.nblk = max(1, (int)(((long long)s.nk + KB - 1) / KB));  // an empty sequence still gets its zeros
+  return s;
+}
+
+// A place in the line of units: block blk of (b, kv head, tile).
+struct Place {
+  int b, kvh, tile, blk;
+  Seq s;
+};
+template <int R, int KB>
+__device__ __forceinline__ void next_seq(const PagedAttnArgs &a, Place &p) {
+  while (++p.b < a.B) {
+    p.s = seq_of<R, KB>(a, p.b);
+    if (p.s.tiles) break;
+  }
+}
+template <int R, int KB>
+__device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n) {
+  p.blk += n;
+  while (p.b < a.B && p.blk >= p.s.nblk) {
+    p.blk -= p.s.nblk;
+    if (++p.tile == p.s.tiles) {
+      p.tile = 0;
+      if (++p.kvh == a.pages.n_kv_heads) {
+        p.kvh = 0;
+        next_seq<R, KB>(a, p);
+      }
+    }
+  }
+}
+
+
+// The range [u0, u1) of a CTA; total units, cut into `ranges` ranges.
+struct Range {
+  long long u0, u1, total;
+  int ranges;
+  bool any;
+  // the range that holds unit u
+  __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * ranges + total - 1) / total) - 1; }
+};
+
+// All W warps of the CTA: the CTA's range, its first place in *place (shared
+// memory; valid for every thread on return).  A range has at least `least`
+// units, the last one aside.
+template <int R, int KB, int W>
+__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place, long long *scan, int least = W) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, KV = a.pages.n_kv_heads;
+  const int per = (a.B + 32 * W - 1) / (32 * W);
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_of<R, KB>(a, b).units(KV);
+  long long x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  Range rg;
+  long long base = 0;
+  rg.total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i == warp) base = rg.total;
+    rg.total += scan[i];
+  }
+  rg.ranges = (int)min((long long)gridDim.x, (rg.total + least - 1) / least);
+  rg.any = (int)blockIdx.x < rg.ranges;
+  rg.u0 = rg.any ? rg.total * blockIdx.x / rg.ranges : 0;
+  rg.u1 = rg.any ? rg.total * (blockIdx.x + 1) / rg.ranges : 0;
+  long long at = base + x - mine;
+  if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
+    Place p;
+    for (p.b = b0; p.b < b1; ++p.b) {
+      p.s = seq_of<R, KB>(a, p.b);
+      if (rg.u0 < at + p.s.units(KV)) break;
+      at += p.s.units(KV);
+    }
+    const long long off = rg.u0 - at;
+    const long long item = off / p.s.nblk;
+    p.blk = (int)(off - item * p.s.nblk);
+    p.kvh = (int)(item / p.s.tiles);
+    p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
+    *place = p;
+  }
+  __syncthreads();
+  return rg;
+}
+
+}  // namespace
+
+// The shares of a launch in the workspace: two per range at most, kr queries each.
+struct ShareBuf {
+  float *o;      // [ranges][2][kr][dp]
+  float2 *ml;    // [ranges][2][kr] (max in log2 units, sum)
+  Share *desc;   // [ranges]
+  ShareBuf(void *ws, int kr, int dp)
+      : o(static_cast<float *>(ws)), ml(reinterpret_cast<float2 *>(o + (size_t)kMaxRanges * 2 * kr * dp)),
+        desc(reinterpret_cast<Share *>(ml + (size_t)kMaxRanges * 2 * kr)) {}
+  static constexpr int64_t bytes(int kr, int dp) {
+    return (int64_t)kMaxRanges * 2 * kr * (dp * 4 + 8) + (int64_t)kMaxRanges * sizeof(Share);
+  }
+};
+
+// k_paged_attn.cu
+bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap, int *head_first);
+cudaError_t paged_grid(int *grid);  // one range per SM
+cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s);
+
+// k_paged_attn_tc.cu: bf16, head_dim <= 128, boxes of box_keys (16 .. 128) slots of one page
+constexpr int kTcQueries = 256;  // queries of a tile
+int tc_box_keys(const dcu_pages &p);  // 0: the pages do not suit
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, void *ws, cudaStream_t s);
+
+}  // namespace dcu

@@ -11,7 +11,10 @@ from tests import paged_ref as R
 pytestmark = pytest.mark.gpu
 
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
-P_STEP = {"bf16": 2.0 ** -16, "f32": 0.0}  # rounding of the softmax weights before P V (bf16 high + low parts)
+# rounding of the softmax weights before P V: bf16 high + low parts, or one bf16 (half a step: 2^-8) on the tensor-core
+# path for many queries
+P_STEP = {"bf16": 2.0 ** -16, "f32": 0.0}
+P_STEP_TC = 2.0 ** -8
 
 
 def i32(x):
@@ -233,11 +236,13 @@ def case_inputs(seed, dtype, H, KV, hd, page, layout, lens, rows, tail=2, q_scal
     return q, start, np.array(lens), table, k, v
 
 
-def check_attention(got, q, start, lens, table, k, v, dtype, scale, p_step=None):
+def check_attention(got, q, start, lens, table, k, v, dtype, scale):
     hd = q.shape[-1]
+    many = dtype == "bf16" and hd <= 128 and q.shape[0] * (q.shape[1] // k.shape[2]) > 32 * len(lens)
+    p_step = P_STEP_TC if many else P_STEP[dtype]
     kn, vn = np.nan_to_num(f64(k), nan=0, posinf=0), np.nan_to_num(f64(v), nan=0, posinf=0)
     want, A, mag = R.attention(f64(q), start, lens, table, kn, vn, scale)
-    tol = R.attention_bound(want, A, mag, DT[dtype], max(1, max(lens)), hd, P_STEP[dtype] if p_step is None else p_step)
+    tol = R.attention_bound(want, A, mag, DT[dtype], max(1, max(lens)), hd, p_step)
     n = int(start[-1])
     err = np.abs(f64(got)[:n] - want[:n])
     assert np.all(np.isfinite(f64(got)[:n]))
@@ -263,6 +268,12 @@ ATTN = [  # H, KV, hd, page, layout, lens, rows
     (3, 3, 32, 16, "slot", [60] * 70, [2] * 70),
     (2, 2, 64, 16, "slot", [0] * 5, [1] * 5),
     (4, 4, 128, 128, "head", [600, 1100], [200, 129]),
+    (8, 1, 128, 16, "slot", [1000, 129, 127, 1, 0, 128, 700], [40, 32, 17, 33, 50, 1, 64]),  # tiles of one and two halves
+    (4, 2, 64, 32, "mixed", [3000, 40, 256], [300, 129, 128]),
+    (2, 2, 112, 256, "slot", [513], [77]),
+    (3, 3, 48, 64, "head", [5000, 64], [65, 256]),
+    (28, 4, 128, 48, "slot", [200, 333], [65, 1]),
+    (32, 32, 128, 64, "slot", [1024], [65]),
 ]
 
 
