@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
   }
 
   // ---- this CTA's range of the units and its first place
-  const Range rg = find_range<R, KB, W>(a, &s_place, s_scan);
+  const Range rg = find_range<R, KB, W>(a, &s_place, s_scan, W);  // at least a block per warp
   if (!rg.any) {
     if (tid == 0) shares[blockIdx.x].last = -1;
     return;
@@ -259,18 +259,19 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
     const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
     const int ngrp = NT == 1 ? 1 : (nq + 7) >> 3;
     // queries of the tile -> shared memory (zeros past nq and past head_dim)
-    {
-      const char *qb = static_cast<const char *>(a.q);
-      for (int i = tid; i < ngrp * 8 * CPR; i += C::kThreads) {
-        const int r = i / CPR, c = i - r * CPR;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (r < nq && c * (16 / C::kEs) < hd) {
-          const int pq = q0 + r, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
-          v = *reinterpret_cast<const uint4 *>(qb + ((size_t)row * a.n_heads + h) * hd * C::kEs + c * 16);
-        }
-        *reinterpret_cast<uint4 *>(q_sm + r * C::kQPitch + c * 16) = v;
-      }
+    for (int i = tid; i < ngrp * 8 * CPR; i += C::kThreads) {
+      const int r = i / CPR, c = i - r * CPR;
+      const bool in = r < nq && c * (16 / C::kEs) < hd;
+      const int pq = q0 + (in ? r : 0), row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+      const char *src = static_cast<const char *>(a.q) +
+                        (((size_t)row * a.n_heads + h) * hd * C::kEs + (in ? c * 16 : 0));
+      uint8_t *dst = q_sm + r * C::kQPitch + c * 16;
+      if constexpr (TMA)
+        load_query16(su32(dst), src, in);
+      else  // (waiting for an asynchronous copy here would drain the ring's)
+        *reinterpret_cast<uint4 *>(dst) = in ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
     }
+    if constexpr (TMA) load_query_wait();
     __syncthreads();
     // B fragments of a single query group stay in registers: dims 32 kk + 8 i of the 8 queries
     [[maybe_unused]] uint32_t qf[F32 || NT > 1 ? 1 : DP / 32][4];
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
       }
     __syncthreads();
     const int slot = s0 == u0 ? 0 : 1;  // the range's first segment, or its last one
-    const size_t pbase = ((size_t)blockIdx.x * 2 + slot) * R;
+    const size_t share = (size_t)blockIdx.x * 2 + slot;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       if (n < ngrp) {
@@ -631,8 +632,8 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
             else
               *reinterpret_cast<uint32_t *>(static_cast<bf16 *>(a.out) + at) = pack2(x0 * inv, x1 * inv);
           } else {
-            *reinterpret_cast<float2 *>(part_o + (pbase + n * 8 + qr) * DP + d) = make_float2(x0, x1);
-            if (d == 0) part_ml[pbase + n * 8 + qr] = make_float2(M, L);
+            *reinterpret_cast<float2 *>(part_o + share_at(share, R, DP, n * 8 + qr, d)) = make_float2(x0, x1);
+            if (d == 0) part_ml[share * R + n * 8 + qr] = make_float2(M, L);
           }
         }
         if (n + 1 < NT) __syncthreads();
@@ -668,46 +669,124 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
   }
 }
 
-// Joins the shares of the item that begins in range blockIdx.x and ends in a
-// later one: shares in range order, w_i = 2^(m_i - M) / sum_i 2^(m_i - M) l_i.
-// The owner's share is its last segment (slot 1, or 0 when that is its only
-// one); the following ranges hold theirs in slot 0.  One warp per query.
+// Joins the shares of the items that range boundaries cut: for a query,
+// out = sum_i w_i O_i, w_i = 2^(m_i - M) / sum_j 2^(m_j - M) l_j, over its
+// shares i.  An item that begins in range r has its first share there (slot 1,
+// or 0 when it is that range's only segment) and the others in slot 0 of the
+// following ranges.  The cut queries of all items form one line, dealt out to
+// the warps of the launch; when there are fewer queries than CTAs (a single
+// token over a long cache: few queries, many shares), a CTA takes a query and
+// its warps split the shares.  Every sum has a fixed order.
+constexpr int kMergeThreads = 256;
+
 template <int DP, class T>
-__global__ void __launch_bounds__(256)
-    k_paged_merge(const __grid_constant__ PagedAttnArgs a, int R, const float *__restrict__ part_o,
+__global__ void __launch_bounds__(kMergeThreads)
+    k_paged_merge(const __grid_constant__ PagedAttnArgs a, int R, int ranges, const float *__restrict__ part_o,
                   const float2 *__restrict__ part_ml, const Share *__restrict__ shares) {
+  constexpr int V = DP == 64 ? 2 : 4, ND = DP == 256 ? 2 : 1;  // dims of a lane: ND vectors of V
+  constexpr int W = kMergeThreads / 32;
   pdl_enter();
-  const Share sh = shares[blockIdx.x];
-  if (sh.last < 0) return;
-  const int lane = threadIdx.x & 31;
+  __shared__ int s_end[kMaxRanges];
+  __shared__ Share s_share[kMaxRanges];
+  __shared__ int s_red[32];
+  __shared__ float s_part[W][DP];
+  __shared__ float2 s_pml[W];
+  static_assert(kMaxRanges <= kMergeThreads, "one thread per range");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int mine = 0;
+  if (tid < ranges) {
+    const Share sh = shares[tid];
+    s_share[tid] = sh;
+    if (sh.last >= 0) mine = sh.nq;
+  }
+  int total;
+  const int pre = block_exclusive_scan(mine, s_red, &total);
+  if (tid < ranges) s_end[tid] = pre + mine;
+  __syncthreads();
   const int G = a.n_heads / a.pages.n_kv_heads, hd = a.pages.head_dim;
-  const int first = blockIdx.x;
-  for (int qr = blockIdx.y * 8 + (threadIdx.x >> 5); qr < sh.nq; qr += gridDim.y * 8) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = first + lane; i <= sh.last; i += 32)
-      M = fmaxf(M, part_ml[((size_t)i * 2 + (i == first ? sh.slot : 0)) * R + qr].x);
-    M = warp_max(M);
-    float acc[DP / 32];
+  const bool whole = total <= (int)gridDim.x;  // a CTA per query
+  const int step = whole ? gridDim.x : gridDim.x * W;
+  for (int i = whole ? blockIdx.x : blockIdx.x * W + warp; i < total; i += step) {
+    int r = 0, z = ranges - 1;  // the first range whose end is above i
+    while (r < z) {
+      const int m = (r + z) >> 1;
+      if (s_end[m] > i) z = m;
+      else r = m + 1;
+    }
+    const Share sh = s_share[r];
+    const int qr = i - (s_end[r] - sh.nq);
+    const int i0 = whole ? r + warp : r, di = whole ? W : 1;
+    // this warp's shares: r + warp, + W, ... or all of them
+    float M = -INFINITY, L = 0.f, acc[ND][V];
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e) acc[e] = 0.f;
+    for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] = 0.f;
+    for (int j0 = i0; j0 <= sh.last; j0 += 32 * di) {
+      const int j = j0 + lane * di;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (j <= sh.last) ml = part_ml[((size_t)j * 2 + (j == r ? sh.slot : 0)) * R + qr];
+      const float m2 = fmaxf(M, warp_max(ml.x));
+      const float f = M == -INFINITY ? 0.f : exp2f(M - m2);
+      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
+      L = L * f + warp_sum(ml.x == -INFINITY ? 0.f : w * ml.y);
+      M = m2;
+#pragma unroll
+      for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] *= f;
+      const int n = min(32, (sh.last - j0) / di + 1);
 #pragma unroll 4
-    for (int i = first; i <= sh.last; ++i) {
-      const size_t at = ((size_t)i * 2 + (i == first ? sh.slot : 0)) * R + qr;
-      const float2 ml = part_ml[at];
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-      L += ml.x == -INFINITY ? 0.f : ml.y * w;
+      for (int k = 0; k < n; ++k) {
+        const int jj = j0 + k * di;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const size_t share = (size_t)jj * 2 + (jj == r ? sh.slot : 0);
 #pragma unroll
-      for (int e = 0; e < DP / 32; ++e) {
-        const int d = lane + 32 * e;
-        if (d < hd) acc[e] += w * part_o[at * DP + d];
+        for (int d = 0; d < ND; ++d) {
+          float v[V];
+          const float *o = part_o + share_at(share, R, DP, qr, d * 128 + lane * V);
+          if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
+          else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (d * 128 + lane * V + e < hd) acc[d][e] += wk * v[e];
+        }
       }
+    }
+    if (whole) {  // join the warps
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s_part[warp][d * 128 + lane * V + e] = acc[d][e];
+      if (lane == 0) s_pml[warp] = make_float2(M, L);
+      __syncthreads();
+      M = -INFINITY;
+      for (int k = 0; k < W; ++k) M = fmaxf(M, s_pml[k].x);
+      L = 0.f;
+#pragma unroll
+      for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] = 0.f;
+      for (int k = 0; k < W; ++k) {
+        const float w = s_pml[k].x == -INFINITY ? 0.f : exp2f(s_pml[k].x - M);
+        L += w * s_pml[k].y;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[d][e] += w * s_part[k][d * 128 + lane * V + e];
+      }
+      __syncthreads();
+      if (warp != 0) continue;
     }
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     const int pq = sh.q0 + qr, row = sh.row0 + pq / G, h = sh.kvh * G + pq % G;
+    T *dst = static_cast<T *>(a.out) + ((size_t)row * a.n_heads + h) * hd;
 #pragma unroll
-    for (int e = 0; e < DP / 32; ++e) {
-      const int d = lane + 32 * e;
-      if (d < hd) static_cast<T *>(a.out)[((size_t)row * a.n_heads + h) * hd + d] = from_f<T>(acc[e] * inv);
+    for (int d = 0; d < ND; ++d) {
+      const int at = d * 128 + lane * V;
+      if (at >= hd) continue;
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+          *reinterpret_cast<uint32_t *>(dst + at + e) = pack2(acc[d][e] * inv, acc[d][e + 1] * inv);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) dst[at + e] = from_f<T>(acc[d][e] * inv);
+      }
     }
   }
 }
@@ -771,8 +850,10 @@ cudaError_t paged_grid(int *grid) {
 
 cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s) {
   const int hd = a.pages.head_dim;
-  const dim3 g(grid, kr / 8 < 4 ? kr / 8 : 4);
-  auto go = [&](auto kern) { return launch_pdl(kern, g, dim3(256), 0, s, a, kr, sb.o, sb.ml, sb.desc); };
+  // four CTAs per SM
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, dim3(4 * grid), dim3(kMergeThreads), 0, s, a, kr, grid, sb.o, sb.ml, sb.desc);
+  };
   if (a.pages.dtype == DCU_F32)
     return hd <= 64 ? go(k_paged_merge<64, float>) : hd <= 128 ? go(k_paged_merge<128, float>)
                                                                : go(k_paged_merge<256, float>);

@@ -7,10 +7,10 @@
 //              box_keys slots x 64 dims (128-byte swizzle), K and V rings of
 //              two stages; a box past the sequence's end or on a bad page is
 //              read at a page coordinate outside the tensor, i.e. as zeros
-//   warp 1     MMA issuer (one thread): S_t = Q_t K^T (M = 128 queries, N = 128
-//              keys) and O_t += P_t V (P_t in tensor memory, V MN-major), for
-//              the tiles t = A, B in turn
-//   warps 2-9 and 10-17  softmax of tile A and of tile B: thread = (query, half
+//   warps 1, 2 MMA issuers of tile A and of tile B (one thread each): S_t =
+//              Q_t K^T (M = 128 queries, N = 128 keys) and O_t += P_t V (P_t in
+//              tensor memory, V MN-major)
+//   warps 4-11 and 12-19  softmax of tile A and of tile B: thread = (query, half
 //              of the chunk's keys)
 //
 // The two tiles share every K and V stage and keep the two engines busy in
@@ -33,7 +33,8 @@ namespace {
 constexpr int kKC = 128;              // keys of a unit
 constexpr int kStages = 2;            // K and V ring depth
 constexpr int kSoftWarps = 8;         // per tile
-constexpr int kWarps = 2 + 2 * kSoftWarps;
+constexpr int kSoft0 = 4;             // first softmax warp
+constexpr int kWarps = kSoft0 + 2 * kSoftWarps;
 constexpr int kThreads = 32 * kWarps;
 
 template <int DP>
@@ -79,6 +80,13 @@ __device__ __forceinline__ void mask32(uint32_t (&r)[32], uint32_t valid) {
     if (!((valid >> c) & 1u)) r[c] = 0xff800000u;  // -inf
 }
 
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_attn_tc(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap kmap,
@@ -87,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries, OC = DP / 2;  // O columns of a half
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * kStages + 9];
+  __shared__ __align__(8) uint64_t bars[4 * kStages + 10];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
@@ -106,18 +114,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto S_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + t); };
   auto P_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + 2 + t); };
   auto PV_DONE = [&](int t) { return bar0 + 8u * (4 * kStages + 4 + t); };
-  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 6), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;
+  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 6), O_FINAL = Q_FULL + 8u;
+  auto DRAIN = [&](int t) { return Q_FULL + 16u + 8u * t; };
 
   if (tid == 0) {
-    for (int s = 0; s < 4 * kStages; ++s) mbar_init(bar0 + 8u * s, 1);
+    // a stage is empty, and a segment final, once both tiles say so (tile A twice where it is alone)
+    for (uint32_t s = 0; s < kStages; ++s) {
+      mbar_init(K_FULL(s), 1);
+      mbar_init(K_EMPTY(s), 2);
+      mbar_init(V_FULL(s), 1);
+      mbar_init(V_EMPTY(s), 2);
+    }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(DRAIN(t), 1);
       mbar_init(S_FULL(t), 1);
       mbar_init(P_FULL(t), kSoftWarps);
       mbar_init(PV_DONE(t), 1);
     }
     mbar_init(Q_FULL, 2 * kSoftWarps);
-    mbar_init(O_FINAL, 1);
-    mbar_init(DRAIN, 1);
+    mbar_init(O_FINAL, 2);
     abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -185,74 +200,94 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t s = issued % kStages;  // a K load whose V was not issued (ends at once if there was none)
       wait_drain(K_FULL(s), (issued / kStages) & 1u);
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16(128, kKC), id_o = idesc_bf16_bmn(128, DP);
-      bool ok = true, any = false;
-      uint32_t g = 0, nseg = 0;          // chunks and segments done
-      uint32_t cnt[2] = {0, 0};          // chunks of each tile done
-      uint32_t pvs[2] = {0, 0};          // PV_DONE phases of each tile
-      auto wait = [&](uint32_t bar, uint32_t par) { return ok = ok && wait_bounded(bar, par & 1u, abort_v, a.status); };
-      auto issue_s = [&](int t, uint32_t st) {
+  } else if (warp == 1 || warp == 2) {
+    // ---- MMA issuer of tile t: the warp runs as one, an elected lane issues
+    const int t = warp - 1;
+    const uint32_t id_s = idesc_bf16(128, kKC), id_o = idesc_bf16_bmn(128, DP);
+    const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + C::kO + 128u * t;
+    const uint64_t qd = sw128_desc(q_s + t * C::kTile), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
+    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
+    bool ok = true, any = false;
+    uint32_t g = 0, cnt = 0, pvs = 0, nseg = 0;  // chunks of the CTA, of this tile, PV_DONE phases, segments
+    auto wait = [&](uint32_t bar, uint32_t par) {
+      ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
+      return ok;
+    };
+    auto issue_s = [&](uint32_t st, bool alone) {
+      const uint64_t kd = kd0 + st * kStep;
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * 16384u;
-          tc_mma(tmem + 128u * t, sw128_desc(q_s + t * C::kTile + off) + (uint64_t)(2 * (kk & 3)),
-                 sw128_desc(k_s + st * C::kTile + off) + (uint64_t)(2 * (kk & 3)), id_s, kk > 0 ? 1u : 0u);
+          const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
+          tc_mma(s_tm, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
         }
-        any = true;
         tc_commit(S_FULL(t));
-      };
-      Place seg = s_place;
-      for (long long s0 = rg.u0; s0 < rg.u1 && ok;) {
-        const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-        const int n = (int)(s1 - s0);
-        const int nt = min(seg.s.tq, seg.s.nq - seg.tile * seg.s.tq) > 128 ? 2 : 1;
-        if (!wait(Q_FULL, nseg) || !wait(K_FULL(g % kStages), g / kStages)) break;
+        tc_commit(K_EMPTY(st));
+        if (alone) tc_commit(K_EMPTY(st));
+      }
+      __syncwarp();
+      any = true;
+    };
+    Place seg = s_place;
+    for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
+      const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
+      const int n = (int)(s1 - s0);
+      const bool alone = min(seg.s.tq, seg.s.nq - seg.tile * seg.s.tq) <= 128;
+      // Every segment in turn, also those tile B sits out: a wait may be at most one phase behind.
+      if (!wait(Q_FULL, nseg)) break;
+      if (t == 1 && alone) {
+        g += (uint32_t)n;
+      } else {
+        if (!wait(K_FULL(g % kStages), g / kStages)) break;
         tc_fence_after();
-        for (int t = 0; t < nt; ++t) issue_s(t, g % kStages);
-        tc_commit(K_EMPTY(g % kStages));
-        for (int j = 0; j < n && ok; ++j, ++g) {
+        issue_s(g % kStages, alone);
+        for (int j = 0; j < n && ok; ++j, ++g, ++cnt) {
           const uint32_t st = g % kStages, st1 = (g + 1) % kStages;
-          for (int t = 0; t < nt && ok; ++t) {
-            if (!wait(P_FULL(t), cnt[t]) || (t == 0 && !wait(V_FULL(st), g / kStages))) break;
-            tc_fence_after();
+          const bool last = j + 1 == n;
+          if (!wait(V_FULL(st), g / kStages) || !wait(P_FULL(t), cnt)) break;
+          // the rows of V past the end of an item's last chunk are cleared by tile A's warps, before its P_FULL
+          if (t == 1 && seg.s.nk - (seg.blk + j) * kKC < kKC && !wait(P_FULL(0), g)) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + st * kStep;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kKC / 16; ++kk)
-              tc_mma_ts(tmem + C::kO + 128u * t, tmem + 128u * t + (uint32_t)((kk >> 2) * 64 + 32 + (kk & 3) * 8),
-                        sw128_mn_desc(v_s + st * C::kTile + (uint32_t)kk * 2048u, 16384u), id_o,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-            if (t == nt - 1) tc_commit(V_EMPTY(st));
-            if (j + 1 < n) {
-              // S_t of the next chunk overwrites P_t: after P_t V has read it
-              tc_commit(PV_DONE(t));
-              if (!wait(PV_DONE(t), pvs[t]++) || (t == 0 && !wait(K_FULL(st1), (g + 1) / kStages))) break;
-              tc_fence_after();
-              issue_s(t, st1);
-              if (t == nt - 1) tc_commit(K_EMPTY(st1));
-            }
-            ++cnt[t];
+              tc_mma_ts(o_tm, s_tm + (uint32_t)((kk >> 2) * 64 + 32 + (kk & 3) * 8), vd + (uint64_t)(kk * (2048 >> 4)),
+                        id_o, (j > 0 || kk > 0) ? 1u : 0u);
+            if (!last) tc_commit(PV_DONE(t));
+            tc_commit(V_EMPTY(st));
+            if (alone) tc_commit(V_EMPTY(st));
+          }
+          __syncwarp();
+          if (!last) {
+            // S_t of the next chunk overwrites P_t: after P_t V has read it
+            if (!wait(K_FULL(st1), (g + 1) / kStages) || !wait(PV_DONE(t), pvs++)) break;
+            tc_fence_after();
+            issue_s(st1, alone);
           }
         }
         if (!ok) break;
-        tc_commit(O_FINAL);
-        ++nseg;
-        advance<R, kKC>(a, seg, n);
-        s0 = s1;
+        if (elect_one()) {
+          tc_commit(O_FINAL);
+          if (alone) tc_commit(O_FINAL);
+        }
+        __syncwarp();
       }
-      if (!ok && any) {
-        tc_commit(DRAIN);
-        wait_drain(DRAIN, 0);
-      }
+      advance<R, kKC>(a, seg, n);
+      s0 = s1;
     }
-  } else {
+    if (!ok && any) {
+      if (elect_one()) tc_commit(DRAIN(t));
+      __syncwarp();
+      wait_drain(DRAIN(t), 0);
+    }
+  } else if (warp >= kSoft0) {
     // ---- softmax
-    const int t = (warp - 2) / kSoftWarps, pt = ((warp - 2) % kSoftWarps) / 4, q4 = warp & 3;
+    const int t = (warp - kSoft0) / kSoftWarps, pt = ((warp - kSoft0) % kSoftWarps) / 4, q4 = warp & 3;
     const int qi = q4 * 32 + lane;                       // query of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_tm = tmem + 128u * t + lane_off, o_tm = tmem + C::kO + 128u * t + lane_off + (uint32_t)(pt * OC);
-    const int st_id = tid - 64;
+    const int st_id = tid - 32 * kSoft0;
     const float sc = a.scale_log2;
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q4) : "memory"); };
     uint32_t cnt = 0, g = 0, nseg = 0;  // chunks of this tile, of the CTA, segments
@@ -271,14 +306,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = nq > 128 ? 256 : 128;
         for (int i = st_id; i < rows * (DP / 8); i += 64 * kSoftWarps) {
           const int r = i / (DP / 8), c = i - r * (DP / 8);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (r < nq && c * 8 < hd) {
-            const int pq = q0 + r, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
-            v = *reinterpret_cast<const uint4 *>(static_cast<const bf16 *>(a.q) + ((size_t)row * a.n_heads + h) * hd +
-                                                 c * 8);
-          }
-          *reinterpret_cast<uint4 *>(sm + (uint32_t)(r >> 7) * C::kTile + tile_off(r & 127, c)) = v;
+          const bool in = r < nq && c * 8 < hd;
+          const int pq = q0 + (in ? r : 0), row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+          load_query16(q_s + (uint32_t)(r >> 7) * C::kTile + tile_off(r & 127, c),
+                       static_cast<const bf16 *>(a.q) + ((size_t)row * a.n_heads + h) * hd + (in ? c * 8 : 0), in);
         }
+        load_query_wait();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(Q_FULL);
@@ -387,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const int pq = q0 + q, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
           bf16 *dst = static_cast<bf16 *>(a.out) + ((size_t)row * a.n_heads + h) * hd + pt * OC;
-          const size_t share = ((size_t)blockIdx.x * 2 + slot) * R + q;
+          const size_t share = (size_t)blockIdx.x * 2 + slot;
           const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
           for (int c = 0; c < OC / 16; ++c) {
@@ -403,14 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     packb(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv),
                                     packb(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv));
               } else {
-                float4 *d = reinterpret_cast<float4 *>(part_o + share * DP + pt * OC + c * 16);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  d[e] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+                  *reinterpret_cast<float4 *>(part_o + share_at(share, R, DP, q, pt * OC + c * 16 + 4 * e)) =
+                      make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
               }
             }
           }
-          if (q < nq && pt == 0 && !(starts && ends)) part_ml[share] = make_float2(m_run, l);
+          if (q < nq && pt == 0 && !(starts && ends)) part_ml[share * R + q] = make_float2(m_run, l);
           tc_fence_before();
         }
         if (s1 == rg.u1 && st_id == 0) {

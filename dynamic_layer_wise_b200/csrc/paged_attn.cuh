@@ -78,25 +78,38 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n)
 }
 
 
-// The range [u0, u1) of a CTA; total units, cut into `ranges` ranges.
+// The range [u0, u1) of a CTA.  Range i of the launch holds q + 1 units when
+// i < rem, else q.
 struct Range {
-  long long u0, u1, total;
-  int ranges;
+  long long u0, u1, q;
+  int rem;
   bool any;
   // the range that holds unit u
-  __device__ __forceinline__ int of(long long u) const { return (int)(((u + 1) * ranges + total - 1) / total) - 1; }
+  __device__ __forceinline__ int of(long long u) const {
+    const long long wide = rem * (q + 1);
+    return u < wide ? (int)(u / (q + 1)) : rem + (int)((u - wide) / q);
+  }
 };
 
+__device__ __forceinline__ long long div_ll(long long a, int b) {
+  return a < (1ll << 32) ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // All W warps of the CTA: the CTA's range, its first place in *place (shared
-// memory; valid for every thread on return).  A range has at least `least`
-// units, the last one aside.
+// memory; valid for every thread on return).  A launch uses as many ranges as
+// have at least `least` units each (the grid at most).
 template <int R, int KB, int W>
-__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place, long long *scan, int least = W) {
+__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place, long long *scan, int least) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, KV = a.pages.n_kv_heads;
   const int per = (a.B + 32 * W - 1) / (32 * W);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_of<R, KB>(a, b).units(KV);
+  Place p;  // with one sequence per thread (B <= 32 W) its items are kept
+  p.b = b0;
+  for (int b = b0; b < b1; ++b) {
+    p.s = seq_of<R, KB>(a, b);
+    mine += p.s.units(KV);
+  }
   long long x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -106,29 +119,29 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
   if (lane == 31) scan[warp] = x;
   __syncthreads();
   Range rg;
-  long long base = 0;
-  rg.total = 0;
+  long long base = 0, total = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    if (i == warp) base = rg.total;
-    rg.total += scan[i];
+    if (i == warp) base = total;
+    total += scan[i];
   }
-  rg.ranges = (int)min((long long)gridDim.x, (rg.total + least - 1) / least);
-  rg.any = (int)blockIdx.x < rg.ranges;
-  rg.u0 = rg.any ? rg.total * blockIdx.x / rg.ranges : 0;
-  rg.u1 = rg.any ? rg.total * (blockIdx.x + 1) / rg.ranges : 0;
+  const int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
+  rg.any = (int)blockIdx.x < ranges;
+  rg.q = ranges ? div_ll(total, ranges) : 0;
+  rg.rem = (int)(total - rg.q * ranges);
+  rg.u0 = rg.any ? blockIdx.x * rg.q + min((int)blockIdx.x, rg.rem) : 0;
+  rg.u1 = rg.any ? rg.u0 + rg.q + ((int)blockIdx.x < rg.rem ? 1 : 0) : 0;
   long long at = base + x - mine;
   if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
-    Place p;
-    for (p.b = b0; p.b < b1; ++p.b) {
-      p.s = seq_of<R, KB>(a, p.b);
-      if (rg.u0 < at + p.s.units(KV)) break;
-      at += p.s.units(KV);
-    }
-    const long long off = rg.u0 - at;
-    const long long item = off / p.s.nblk;
+    if (per > 1)
+      for (p.b = b0; p.b < b1; ++p.b) {
+        p.s = seq_of<R, KB>(a, p.b);
+        if (rg.u0 < at + p.s.units(KV)) break;
+        at += p.s.units(KV);
+      }
+    const long long off = rg.u0 - at, item = div_ll(off, p.s.nblk);
     p.blk = (int)(off - item * p.s.nblk);
-    p.kvh = (int)(item / p.s.tiles);
+    p.kvh = (int)div_ll(item, p.s.tiles);
     p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
     *place = p;
   }
@@ -136,11 +149,21 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
   return rg;
 }
 
+// Place of dims d .. d + 7 of query q in a share of kr queries: groups of 8
+// dims, so a warp of queries and a warp of dims both touch whole sectors.
+__device__ __forceinline__ size_t share_at(size_t share, int kr, int dp, int q, int d) {
+  return ((share * (dp / 8) + d / 8) * kr + q) * 8 + (d & 7);
+}
+__device__ __forceinline__ void load_query16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void load_query_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 }  // namespace
 
 // The shares of a launch in the workspace: two per range at most, kr queries each.
 struct ShareBuf {
-  float *o;      // [ranges][2][kr][dp]
+  float *o;      // [ranges][2][dp / 8][kr][8]
   float2 *ml;    // [ranges][2][kr] (max in log2 units, sum)
   Share *desc;   // [ranges]
   ShareBuf(void *ws, int kr, int dp)
