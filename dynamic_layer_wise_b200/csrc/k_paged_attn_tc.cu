@@ -11,13 +11,16 @@
 //              Q_t K^T (M = 128 queries, N = 128 keys) and O_t += P_t V (P_t in
 //              tensor memory, V MN-major)
 //   warps 4-11 and 12-19  softmax of tile A and of tile B: thread = (query, half
-//              of the chunk's keys)
+//              of the sub-chunk's keys)
 //
-// The two tiles share every K and V stage and keep the two engines busy in
-// turn: while the softmax of one tile runs, the tensor core works for the other.
-// TMEM: S_A, S_B, O_A, O_B of 128 columns each; each half's P_t (bf16 pairs)
-// overwrites scores that its threads have read, and S_t of the next chunk waits
-// for P_t V.
+// A chunk is worked in two sub-chunks of 64 keys, each with a TMEM score buffer
+// of its own per tile, so S of the next sub-chunk is there when the softmax
+// gets to it and only the softmax is on the critical path; the two tiles share
+// every K and V stage.  An item of at most 128 queries gives both tiles the
+// same queries and every other chunk, each with its own maximum, sum and O, and
+// the two are joined at its end.
+// TMEM: two score buffers of 64 columns for A, two for B, O_A and O_B of 128
+// columns; P (bf16 pairs) overwrites scores that the same thread has read.
 // P is rounded to bf16 once, as in the dense attention of a step: a second
 // product for the low part would cost half as much again on the pipe that
 // bounds this kernel.
@@ -31,6 +34,7 @@ namespace dcu {
 namespace {
 
 constexpr int kKC = 128;              // keys of a unit
+constexpr int kSub = 64;              // keys of a sub-chunk
 constexpr int kStages = 2;            // K and V ring depth
 constexpr int kSoftWarps = 8;         // per tile
 constexpr int kSoft0 = 4;             // first softmax warp
@@ -66,20 +70,6 @@ __device__ __forceinline__ uint32_t packb(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// Valid keys of a half chunk as two words: the first nv keys, less the boxes in `bad`.
-__device__ __forceinline__ uint2 valid_keys(int nv, uint32_t bad, int box) {
-  unsigned long long m = nv >= 64 ? ~0ull : nv <= 0 ? 0ull : (1ull << nv) - 1ull;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if ((bad >> i) & 1u) m &= ~((box >= 64 ? ~0ull : (1ull << box) - 1ull) << (i * box & 63));
-  return make_uint2((uint32_t)m, (uint32_t)(m >> 32));
-}
-__device__ __forceinline__ void mask32(uint32_t (&r)[32], uint32_t valid) {
-#pragma unroll
-  for (int c = 0; c < 32; ++c)
-    if (!((valid >> c) & 1u)) r[c] = 0xff800000u;  // -inf
-}
-
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -95,13 +85,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries, OC = DP / 2;  // O columns of a half
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * kStages + 10];
+  __shared__ __align__(8) uint64_t bars[4 * kStages + 15];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
   __shared__ Place s_place;
-  __shared__ float s_mx[2][2][2][128];  // [chunk parity][tile][half] maximum of the half's keys
+  __shared__ float s_mx[2][2][2][128];  // [sub-chunk parity][tile][half] maximum of the half's keys
   __shared__ float s_l[2][2][128];      // [tile][half] share of the row sum
+  __shared__ float s_m[2][128];         // [tile] final row maximum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
@@ -111,14 +102,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto K_EMPTY = [&](uint32_t s) { return bar0 + 8u * (kStages + s); };
   auto V_FULL = [&](uint32_t s) { return bar0 + 8u * (2 * kStages + s); };
   auto V_EMPTY = [&](uint32_t s) { return bar0 + 8u * (3 * kStages + s); };
-  auto S_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + t); };
-  auto P_FULL = [&](int t) { return bar0 + 8u * (4 * kStages + 2 + t); };
-  auto PV_DONE = [&](int t) { return bar0 + 8u * (4 * kStages + 4 + t); };
-  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 6), O_FINAL = Q_FULL + 8u;
-  auto DRAIN = [&](int t) { return Q_FULL + 16u + 8u * t; };
+  auto S_FULL = [&](int t, uint32_t b) { return bar0 + 8u * (4 * kStages + 2 * t + b); };
+  auto P_FULL = [&](int t, uint32_t b) { return bar0 + 8u * (4 * kStages + 4 + 2 * t + b); };
+  auto PV_DONE = [&](int t) { return bar0 + 8u * (4 * kStages + 8 + t); };
+  auto DRAIN = [&](int t) { return bar0 + 8u * (4 * kStages + 10 + t); };
+  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 12), O_FINAL = Q_FULL + 8u;
+  // tile A's softmax warps, per segment of two tiles whose last chunk ends inside a page: V's rows there are cleared.
+  // (Tile B may be a chunk ahead or behind, so P_FULL of tile A would not do: a parity wait is only sound within one
+  // phase.)
+  const uint32_t V_CLEAR = Q_FULL + 16u;
 
   if (tid == 0) {
-    // a stage is empty, and a segment final, once both tiles say so (tile A twice where it is alone)
+    // a stage is empty, and a segment final, once both tiles say so (a tile that has the chunk to itself, twice)
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(K_FULL(s), 1);
       mbar_init(K_EMPTY(s), 2);
@@ -127,12 +122,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(DRAIN(t), 1);
-      mbar_init(S_FULL(t), 1);
-      mbar_init(P_FULL(t), kSoftWarps);
+      for (uint32_t b = 0; b < 2; ++b) {
+        mbar_init(S_FULL(t, b), 1);
+        mbar_init(P_FULL(t, b), kSoftWarps);
+      }
       mbar_init(PV_DONE(t), 1);
     }
     mbar_init(Q_FULL, 2 * kSoftWarps);
     mbar_init(O_FINAL, 2);
+    mbar_init(V_CLEAR, kSoftWarps);
     abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -203,27 +201,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1 || warp == 2) {
     // ---- MMA issuer of tile t: the warp runs as one, an elected lane issues
     const int t = warp - 1;
-    const uint32_t id_s = idesc_bf16(128, kKC), id_o = idesc_bf16_bmn(128, DP);
+    const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
     const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + C::kO + 128u * t;
-    const uint64_t qd = sw128_desc(q_s + t * C::kTile), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
-    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
+    const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
+    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages (and of the Q tiles)
     bool ok = true, any = false;
-    uint32_t g = 0, cnt = 0, pvs = 0, nseg = 0;  // chunks of the CTA, of this tile, PV_DONE phases, segments
+    uint32_t g = 0, nseg = 0;      // chunks of the CTA, segments
+    uint32_t u = 0, clears = 0;    // sub-chunks of this tile, V_CLEAR phases
     auto wait = [&](uint32_t bar, uint32_t par) {
       ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
       return ok;
     };
-    auto issue_s = [&](uint32_t st, bool alone) {
-      const uint64_t kd = kd0 + st * kStep;
+    // scores of sub-chunk h of the chunk in stage st, into buffer h
+    auto issue_s = [&](uint32_t st, uint32_t h, bool alone) {
+      const uint64_t kd = kd0 + st * kStep + h * (uint64_t)(kSub * 128 >> 4), qq = alone ? qd : qd + t * kStep;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
-          tc_mma(s_tm, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+          tc_mma(s_tm + h * 64u, qq + off, kd + off, id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(S_FULL(t));
-        tc_commit(K_EMPTY(st));
-        if (alone) tc_commit(K_EMPTY(st));
+        tc_commit(S_FULL(t, h));
+        if (h) {
+          tc_commit(K_EMPTY(st));
+          if (alone) tc_commit(K_EMPTY(st));
+        }
       }
       __syncwarp();
       any = true;
@@ -233,46 +235,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
       const int n = (int)(s1 - s0);
       const bool alone = min(seg.s.tq, seg.s.nq - seg.tile * seg.s.tq) <= 128;
-      // Every segment in turn, also those tile B sits out: a wait may be at most one phase behind.
+      const int j0 = alone ? t : 0, dj = alone ? 2 : 1;  // this tile's chunks: j0, j0 + dj, ...
+      // every segment in turn, also one without a chunk of this tile: a wait may be at most one phase behind
       if (!wait(Q_FULL, nseg)) break;
-      if (t == 1 && alone) {
-        g += (uint32_t)n;
-      } else {
-        if (!wait(K_FULL(g % kStages), g / kStages)) break;
+      if (j0 < n) {
+        const uint32_t st = (g + j0) % kStages;
+        if (!wait(K_FULL(st), (g + j0) / kStages)) break;
         tc_fence_after();
-        issue_s(g % kStages, alone);
-        for (int j = 0; j < n && ok; ++j, ++g, ++cnt) {
-          const uint32_t st = g % kStages, st1 = (g + 1) % kStages;
-          const bool last = j + 1 == n;
-          if (!wait(V_FULL(st), g / kStages) || !wait(P_FULL(t), cnt)) break;
-          // the rows of V past the end of an item's last chunk are cleared by tile A's warps, before its P_FULL
-          if (t == 1 && seg.s.nk - (seg.blk + j) * kKC < kKC && !wait(P_FULL(0), g)) break;
+        issue_s(st, 0, alone);
+        issue_s(st, 1, alone);
+      }
+      for (int j = j0; j < n && ok; j += dj) {
+        const uint32_t gj = g + (uint32_t)j, st = gj % kStages, gn = gj + (uint32_t)dj, sn = gn % kStages;
+        const bool last = j + dj >= n;
+        for (uint32_t h = 0; h < 2; ++h, ++u) {
+          if (!wait(P_FULL(t, h), u >> 1)) break;
+          if (h == 0) {
+            if (!wait(V_FULL(st), gj / kStages)) break;
+            // the rows of V past the end of an item's last chunk are cleared by the softmax warps of tile A, or of the
+            // one tile that takes the chunk, before their P_FULL (tile B: V_CLEAR)
+            if (!alone && t == 1 && seg.s.nk - (seg.blk + j) * kKC < kKC && !wait(V_CLEAR, clears++)) break;
+          }
           tc_fence_after();
-          const uint64_t vd = vd0 + st * kStep;
+          const uint64_t vd = vd0 + st * kStep + h * (uint64_t)(kSub * 128 >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kKC / 16; ++kk)
-              tc_mma_ts(o_tm, s_tm + (uint32_t)((kk >> 2) * 64 + 32 + (kk & 3) * 8), vd + (uint64_t)(kk * (2048 >> 4)),
-                        id_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (!last) tc_commit(PV_DONE(t));
-            tc_commit(V_EMPTY(st));
-            if (alone) tc_commit(V_EMPTY(st));
+            for (int kk = 0; kk < kSub / 16; ++kk)
+              tc_mma_ts(o_tm, s_tm + h * 64u + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8),
+                        vd + (uint64_t)(kk * (2048 >> 4)), id_o, (j > j0 || h > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(PV_DONE(t));
+            if (h) {
+              tc_commit(V_EMPTY(st));
+              if (alone) tc_commit(V_EMPTY(st));
+            }
           }
           __syncwarp();
+          // the buffer's next scores overwrite P: after P V has read it
+          if ((!last && h == 0 && !wait(K_FULL(sn), gn / kStages)) || !wait(PV_DONE(t), u)) break;
           if (!last) {
-            // S_t of the next chunk overwrites P_t: after P_t V has read it
-            if (!wait(K_FULL(st1), (g + 1) / kStages) || !wait(PV_DONE(t), pvs++)) break;
             tc_fence_after();
-            issue_s(st1, alone);
+            issue_s(sn, h, alone);
           }
         }
-        if (!ok) break;
-        if (elect_one()) {
-          tc_commit(O_FINAL);
-          if (alone) tc_commit(O_FINAL);
-        }
-        __syncwarp();
       }
+      if (!ok) break;
+      if (elect_one()) tc_commit(O_FINAL);
+      __syncwarp();
+      g += (uint32_t)n;
       advance<R, kKC>(a, seg, n);
       s0 = s1;
     }
@@ -290,16 +299,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st_id = tid - 32 * kSoft0;
     const float sc = a.scale_log2;
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q4) : "memory"); };
-    uint32_t cnt = 0, g = 0, nseg = 0;  // chunks of this tile, of the CTA, segments
+    uint32_t u = 0, g = 0, nseg = 0;  // sub-chunks of this tile, chunks of the CTA, segments
     bool alive = true;
-    const int nbh = 64 / box > 0 ? 64 / box : 1;  // boxes of a half (a box of 128 slots spans both)
+    constexpr int kPart = kSub / 2;   // keys of a thread in a sub-chunk
     Place seg = s_place;
     for (long long s0 = rg.u0; s0 < rg.u1; ++nseg) {
       const Seq &sq = seg.s;
       const long long s1 = min(rg.u1, s0 + (sq.nblk - seg.blk));
       const int n = (int)(s1 - s0);
       const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
-      const bool on = t == 0 || nq > 128;
+      const bool alone = nq <= 128;
+      const int j0 = alone ? t : 0, dj = alone ? 2 : 1;  // this tile's chunks: j0, j0 + dj, ...
       // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read
       // theirs (O_FINAL)
       {
@@ -316,149 +326,172 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(Q_FULL);
       }
-      if (on) {
-        float m_run = -INFINITY, l_run = 0.f;
-        // the pages of this half's boxes, looked up a chunk ahead
-        auto look = [&](int blk) {
-          const int key = blk * kKC + pt * 64 + lane * box;
-          return lane < nbh && key < sq.nk ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)] : 0;
-        };
-        int pg = look(seg.blk);
-        for (int j = 0; j < n; ++j) {
-          const int key0 = (seg.blk + j) * kKC;
-          const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.pages.n_pages);
-          if (j + 1 < n) pg = look(seg.blk + j + 1);
-          if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(t), cnt & 1u, abort_v, a.status));
-          const int nv = sq.nk - key0 - pt * 64;  // valid keys of this half
-          // Raw scores: the scale (> 0) commutes with the maximum and enters the exponent.  The first 32 keys are read
-          // again for the exponentials rather than kept, which holds the thread within 96 registers.
-          const bool cut = nv < 64 || bad;
-          const uint2 valid = cut ? valid_keys(nv, bad, box) : make_uint2(~0u, ~0u);
-          uint32_t sr[32];
-          float mc = -INFINITY;
-          if (alive) {
-            tc_fence_after();
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              tmem_ld32_issue(s_tm + (uint32_t)(pt * 64 + hf * 32), sr);
-              tmem_wait_ld_tie32(sr);
-              if (cut) mask32(sr, hf ? valid.y : valid.x);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
-            }
-            mc = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          }
-          s_mx[cnt & 1][t][pt][qi] = mc;
-          pair_sync();
-          mc = fmaxf(mc, s_mx[cnt & 1][t][1 - pt][qi]);
-          ++cnt;
-          const uint32_t gj = g + (uint32_t)j;
-          if (!alive) continue;
-          // The maximum moves only when a chunk exceeds it by more than 8 (log2 units): P stays below 2^8, most
-          // chunks rescale nothing, and P, the sum and O share it.
-          const bool grow = mc > m_run + 8.f;
-          const float m_new = grow ? mc : m_run;
-          const float alpha = grow ? (m_run == -INFINITY ? 0.f : ex2a(m_run - m_new)) : 1.f;
-          if (j > 0 && __any_sync(0xffffffffu, grow)) {  // P V of the last chunk is complete: S_FULL follows it
-#pragma unroll 1
-            for (int c = 0; c < OC / 16; ++c) {
-              float ov[16];
-              tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] *= alpha;
-              tmem_st16(o_tm + (uint32_t)(c * 16), ov);
-            }
-          }
-          m_run = m_new;
-          const float m_use = m_new == -INFINITY ? 0.f : m_new;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
-          // P of this half goes over its own scores of keys 32 .. 63, which are in registers by then: columns 64 pt + 32 .. + 64
-          // (16 per 32 keys)
-#pragma unroll
-          for (int hf = 1; hf >= 0; --hf) {
-            if (hf == 0) {
-              tmem_ld32_issue(s_tm + (uint32_t)(pt * 64), sr);
-              tmem_wait_ld_tie32(sr);
-              if (cut) mask32(sr, valid.x);
-            }
-            uint32_t pk[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float p0 = ex2a(fmaf(__uint_as_float(sr[2 * c]), sc, -m_use));
-              const float p1 = ex2a(fmaf(__uint_as_float(sr[2 * c + 1]), sc, -m_use));
-              ps[c & 3] += p0 + p1;
-              pk[c] = packb(p0, p1);
-            }
-            tmem_st16u(s_tm + (uint32_t)(pt * 64 + (hf ? 48 : 32)), pk);
-          }
-          l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-          if (t == 0 && sq.nk - key0 < kKC) {
-            // past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
-            // zeros; the rows are cleared after the copy and before P_FULL lets P V start.
-            alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(gj % kStages), (gj / kStages) & 1u, abort_v, a.status));
-            if (!alive) continue;
-            const int r0 = max(sq.nk - key0, 0), r1 = min(kKC, (r0 + box - 1) / box * box);
-            for (int i = st_id; i < (r1 - r0) * (DP / 8); i += 32 * kSoftWarps)
-              *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kStages) * C::kTile +
-                                         tile_off(r0 + i / (DP / 8), i % (DP / 8))) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(P_FULL(t));
-        }
-        // ---- the segment's end
-        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
-        s_l[t][pt][qi] = l_run;
-        pair_sync();
-        const float l = s_l[t][0][qi] + s_l[t][1][qi];
-        const bool starts = seg.blk == 0, ends = n == sq.nblk - seg.blk;
-        const int slot = s0 == rg.u0 ? 0 : 1, q = t * 128 + qi;
+      float m_run = -INFINITY, l_run = 0.f;
+      // the pages of this thread's keys of a sub-chunk (two boxes of 16 slots at most), looked up one ahead
+      auto look = [&](int key) {
+        key += pt * kPart + lane * box;
+        return lane < 2 && lane * box < kPart && key < sq.nk
+                   ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)]
+                   : 0;
+      };
+      const int ns = j0 < n ? 2 * ((n - j0 + dj - 1) / dj) : 0;  // this tile's sub-chunks
+      int pg = ns ? look((seg.blk + j0) * kKC) : 0;
+      for (int i = 0; i < ns; ++i, ++u) {
+        const int j = j0 + (i >> 1) * dj, key0 = (seg.blk + j) * kKC + (i & 1) * kSub;
+        const uint32_t hb = (uint32_t)(i & 1), s_buf = s_tm + hb * 64u;
+        const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.pages.n_pages);
+        if (i + 1 < ns) pg = look((seg.blk + j0 + ((i + 1) >> 1) * dj) * kKC + ((i + 1) & 1) * kSub);
+        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(t, hb), (u >> 1) & 1u, abort_v, a.status));
+        const int nv = sq.nk - key0 - pt * kPart;  // valid keys of this thread
+        uint32_t sr[kPart];  // raw scores: the scale (> 0) commutes with the maximum and enters the exponent
+        float mc = -INFINITY;
         if (alive) {
           tc_fence_after();
-          const int pq = q0 + q, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
-          bf16 *dst = static_cast<bf16 *>(a.out) + ((size_t)row * a.n_heads + h) * hd + pt * OC;
-          const size_t share = (size_t)blockIdx.x * 2 + slot;
-          const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+          tmem_ld32_issue(s_buf + (uint32_t)(pt * kPart), sr);
+          tmem_wait_ld_tie32(sr);
+          if (nv < kPart || bad) {
+            uint32_t valid = nv >= kPart ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
+            if (bad & 1u) valid &= box >= kPart ? 0u : ~0u << box;
+            if (bad & 2u) valid &= (1u << box) - 1u;
 #pragma unroll
+            for (int c = 0; c < kPart; ++c)
+              if (!((valid >> c) & 1u)) sr[c] = 0xff800000u;  // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kPart; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
+          mc = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        }
+        s_mx[u & 1][t][pt][qi] = mc;
+        pair_sync();
+        mc = fmaxf(mc, s_mx[u & 1][t][1 - pt][qi]);
+        if (!alive) continue;
+        // The maximum moves only when a sub-chunk exceeds it by more than 8 (log2 units): P stays below 2^8, most
+        // sub-chunks rescale nothing, and P, the sum and O share it.
+        const bool grow = mc > m_run + 8.f;
+        const float m_new = grow ? mc : m_run;
+        const float alpha = grow ? (m_run == -INFINITY ? 0.f : ex2a(m_run - m_new)) : 1.f;
+        if (i > 0 && __any_sync(0xffffffffu, grow)) {
+          // P V of the sub-chunk before must be in O.  The wait is within a phase: P V of the one before that was
+          // complete before S_FULL, and this one's cannot be before its P_FULL.
+          alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE(t), (u - 1) & 1u, abort_v, a.status));
+          if (!alive) continue;
+          tc_fence_after();
+#pragma unroll 1
           for (int c = 0; c < OC / 16; ++c) {
             float ov[16];
             tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
-            if (q < nq && pt * OC + c * 16 < hd) {
-              if (starts && ends) {
-                uint4 *d = reinterpret_cast<uint4 *>(dst + c * 16);
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  d[e] = make_uint4(packb(ov[8 * e] * inv, ov[8 * e + 1] * inv),
-                                    packb(ov[8 * e + 2] * inv, ov[8 * e + 3] * inv),
-                                    packb(ov[8 * e + 4] * inv, ov[8 * e + 5] * inv),
-                                    packb(ov[8 * e + 6] * inv, ov[8 * e + 7] * inv));
-              } else {
+            for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+            tmem_st16(o_tm + (uint32_t)(c * 16), ov);
+          }
+        }
+        m_run = m_new;
+        const float m_use = m_new == -INFINITY ? 0.f : m_new;
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  *reinterpret_cast<float4 *>(part_o + share_at(share, R, DP, q, pt * OC + c * 16 + 4 * e)) =
-                      make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
-              }
+        for (int c = 0; c < kPart / 2; ++c) {
+          const float p0 = ex2a(fmaf(__uint_as_float(sr[2 * c]), sc, -m_use));
+          const float p1 = ex2a(fmaf(__uint_as_float(sr[2 * c + 1]), sc, -m_use));
+          ps[c & 3] += p0 + p1;
+          sr[c] = packb(p0, p1);
+        }
+        // P: 16 columns over the upper half of this thread's own scores
+        tmem_st16u(s_buf + (uint32_t)(pt * kPart + 16), sr);
+        l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        if (hb == 0 && (alone || t == 0) && sq.nk - key0 < kKC) {
+          // past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
+          // zeros; the rows are cleared after the copy and before P_FULL lets P V start.
+          const uint32_t gj = g + (uint32_t)j;
+          alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(gj % kStages), (gj / kStages) & 1u, abort_v, a.status));
+          if (!alive) continue;
+          const int r0 = max(sq.nk - key0, 0), r1 = min(kKC, (r0 + box - 1) / box * box);
+          for (int w = st_id & (32 * kSoftWarps - 1); w < (r1 - r0) * (DP / 8); w += 32 * kSoftWarps)
+            *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kStages) * C::kTile +
+                                       tile_off(r0 + w / (DP / 8), w % (DP / 8))) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (!alone && lane == 0) mbar_arrive(V_CLEAR);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(P_FULL(t, hb));
+      }
+      // ---- the segment's end
+      if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
+      s_l[t][pt][qi] = l_run;
+      if (pt == 0) s_m[t][qi] = m_run;
+      const bool starts = seg.blk == 0, ends = n == sq.nblk - seg.blk;
+      const int slot = s0 == rg.u0 ? 0 : 1;
+      const size_t share = (size_t)blockIdx.x * 2 + slot;
+      // O columns of this thread, and its query: tiles of their own, half a row per thread; alone, the four threads of
+      // a row take a quarter each of both O's (fa, fb: their weights)
+      int q, c0, nc;
+      float m, l, fa = 1.f, fb = 0.f;
+      if (alone) {
+        asm volatile("bar.sync %0, 128;" ::"r"(9 + q4) : "memory");
+        const float ma = s_m[0][qi], mb = s_m[1][qi];
+        m = fmaxf(ma, mb);
+        fa = ma == -INFINITY ? 0.f : ex2a(ma - m);
+        fb = mb == -INFINITY ? 0.f : ex2a(mb - m);
+        l = (s_l[0][0][qi] + s_l[0][1][qi]) * fa + (s_l[1][0][qi] + s_l[1][1][qi]) * fb;
+        q = qi;
+        nc = DP / 4;
+        c0 = (2 * pt + t) * nc;
+      } else {
+        pair_sync();
+        m = m_run;
+        l = s_l[t][0][qi] + s_l[t][1][qi];
+        q = t * 128 + qi;
+        nc = DP / 2;
+        c0 = pt * nc;
+      }
+      if (alive) {
+        tc_fence_after();
+        const int pq = q0 + q, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
+        bf16 *dst = static_cast<bf16 *>(a.out) + ((size_t)row * a.n_heads + h) * hd;
+        const float inv = starts && ends ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+        const uint32_t oa = tmem + C::kO + (alone ? 0u : 128u * t) + lane_off;
+#pragma unroll 1
+        for (int c = c0; c < c0 + nc; c += 16) {
+          float ov[16];
+          tmem_ld16(oa + (uint32_t)c, ov);
+          if (alone) {
+            float ob[16];
+            if (n > 1) tmem_ld16(oa + 128u + (uint32_t)c, ob);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = n > 1 ? ov[e] * fa + ob[e] * fb : ov[e];
+          }
+          if (q < nq && c < hd) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] *= inv;
+            if (starts && ends) {
+              uint4 *d = reinterpret_cast<uint4 *>(dst + c);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                d[e] = make_uint4(packb(ov[8 * e], ov[8 * e + 1]), packb(ov[8 * e + 2], ov[8 * e + 3]),
+                                  packb(ov[8 * e + 4], ov[8 * e + 5]), packb(ov[8 * e + 6], ov[8 * e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4 *>(part_o + share_at(share, R, DP, q, c + 4 * e)) =
+                    make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
             }
           }
-          if (q < nq && pt == 0 && !(starts && ends)) part_ml[share * R + q] = make_float2(m_run, l);
-          tc_fence_before();
         }
-        if (s1 == rg.u1 && st_id == 0) {
-          Share sh;
-          sh.last = starts && !ends && alive ? rg.of(s0 + sq.nblk - 1) : -1;
-          sh.row0 = sq.row0;
-          sh.q0 = q0;
-          sh.nq = nq;
-          sh.kvh = seg.kvh;
-          sh.slot = slot;
-          shares[blockIdx.x] = sh;
-        }
-      } else {
-        // tile B sits this segment out; its queries' buffer is not rewritten before the segment's MMAs are done
-        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
+        if (q < nq && c0 == 0 && !(starts && ends)) part_ml[share * R + q] = make_float2(m, l);
+        tc_fence_before();
+      }
+      if (s1 == rg.u1 && st_id == 0) {
+        Share sh;
+        sh.last = starts && !ends && alive ? rg.of(s0 + sq.nblk - 1) : -1;
+        sh.row0 = sq.row0;
+        sh.q0 = q0;
+        sh.nq = nq;
+        sh.kvh = seg.kvh;
+        sh.slot = slot;
+        shares[blockIdx.x] = sh;
       }
       g += (uint32_t)n;
       advance<R, kKC>(a, seg, n);

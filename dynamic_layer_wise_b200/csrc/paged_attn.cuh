@@ -78,14 +78,20 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n)
 }
 
 
-// The range [u0, u1) of a CTA.  Range i of the launch holds q + 1 units when
-// i < rem, else q.
+// The range [u0, u1) of a CTA.  Either the line is cut evenly (range i of the
+// launch holds q + 1 units when i < rem, else q), or, for one sequence whose
+// items are few, every item of q units is cut into `parts` ranges: then no CTA
+// works on two items, and an item has fewer shares.
 struct Range {
   long long u0, u1, q;
-  int rem;
+  int rem, parts;  // parts 0: the even cut
   bool any;
   // the range that holds unit u
   __device__ __forceinline__ int of(long long u) const {
+    if (parts) {
+      const long long item = u / q;
+      return (int)(item * parts + ((u - item * q + 1) * parts - 1) / q);
+    }
     const long long wide = rem * (q + 1);
     return u < wide ? (int)(u / (q + 1)) : rem + (int)((u - wide) / q);
   }
@@ -125,12 +131,34 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
     if (i == warp) base = total;
     total += scan[i];
   }
-  const int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
-  rg.any = (int)blockIdx.x < ranges;
-  rg.q = ranges ? div_ll(total, ranges) : 0;
-  rg.rem = (int)(total - rg.q * ranges);
-  rg.u0 = rg.any ? blockIdx.x * rg.q + min((int)blockIdx.x, rg.rem) : 0;
-  rg.u1 = rg.any ? rg.u0 + rg.q + ((int)blockIdx.x < rg.rem ? 1 : 0) : 0;
+  int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
+  const int bid = (int)blockIdx.x;
+  rg.parts = 0;
+  if (a.B == 1 && total > 0) {
+    // cut item by item when that adds no more to the longest range than `least` units, which a second item would cost
+    const Seq s = seq_of<R, KB>(a, 0);
+    const long long items = (long long)KV * s.tiles;
+    if (items <= ranges) {
+      const int f = ranges / (int)items;
+      if ((s.nblk + f - 1) / f <= (int)div_ll(total + ranges - 1, ranges) + least) {
+        rg.parts = f;
+        ranges = (int)items * f;
+        rg.any = bid < ranges;
+        rg.q = s.nblk;
+        rg.rem = 0;
+        const int item = bid / f, part = bid - item * f;
+        rg.u0 = (long long)item * s.nblk + div_ll((long long)part * s.nblk, f);
+        rg.u1 = (long long)item * s.nblk + div_ll((long long)(part + 1) * s.nblk, f);
+      }
+    }
+  }
+  if (!rg.parts) {
+    rg.any = bid < ranges;
+    rg.q = ranges ? div_ll(total, ranges) : 0;
+    rg.rem = (int)(total - rg.q * ranges);
+    rg.u0 = bid * rg.q + min(bid, rg.rem);
+    rg.u1 = rg.u0 + rg.q + (bid < rg.rem ? 1 : 0);
+  }
   long long at = base + x - mine;
   if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
     if (per > 1)
@@ -149,10 +177,10 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
   return rg;
 }
 
-// Place of dims d .. d + 7 of query q in a share of kr queries: groups of 8
-// dims, so a warp of queries and a warp of dims both touch whole sectors.
+// Place of dim d of query q in a share of kr queries: groups of 4 dims, so the
+// threads that write a share (one query each) store whole lines.
 __device__ __forceinline__ size_t share_at(size_t share, int kr, int dp, int q, int d) {
-  return ((share * (dp / 8) + d / 8) * kr + q) * 8 + (d & 7);
+  return ((share * (dp / 4) + d / 4) * kr + q) * 4 + (d & 3);
 }
 __device__ __forceinline__ void load_query16(uint32_t dst, const void *src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
@@ -163,7 +191,7 @@ __device__ __forceinline__ void load_query_wait() { asm volatile("cp.async.wait_
 
 // The shares of a launch in the workspace: two per range at most, kr queries each.
 struct ShareBuf {
-  float *o;      // [ranges][2][dp / 8][kr][8]
+  float *o;      // [ranges][2][dp / 4][kr][4]
   float2 *ml;    // [ranges][2][kr] (max in log2 units, sum)
   Share *desc;   // [ranges]
   ShareBuf(void *ws, int kr, int dp)
