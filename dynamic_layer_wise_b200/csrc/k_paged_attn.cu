@@ -148,13 +148,13 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
   }
 
   // ---- this CTA's range of the units and its first place
-  const Range rg = find_range<R, KB, W>(a, &s_place, s_scan, W);  // at least a block per warp
+  Place seg;  // start of the current segment (the part of an item inside the range)
+  const Range rg = find_range<R, KB, W>(a, seg, &s_place, s_scan, W);  // at least a block per warp
   if (!rg.any) {
     if (tid == 0) shares[blockIdx.x].last = -1;
     return;
   }
   const long long u0 = rg.u0, u1 = rg.u1;
-  Place seg = s_place;  // start of the current segment (the part of an item inside the range)
 
   uint8_t *sm = sm_raw + ((1024u - (su32(sm_raw) & 1023u)) & 1023u);
   const uint32_t sm32 = su32(sm);
@@ -258,13 +258,13 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
     const long long s1 = min(u1, s0 + (sq.nblk - seg.blk));
     const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
     const int ngrp = NT == 1 ? 1 : (nq + 7) >> 3;
+    const Pairs pairs(sq, q0, G);
     // queries of the tile -> shared memory (zeros past nq and past head_dim)
     for (int i = tid; i < ngrp * 8 * CPR; i += C::kThreads) {
       const int r = i / CPR, c = i - r * CPR;
       const bool in = r < nq && c * (16 / C::kEs) < hd;
-      const int pq = q0 + (in ? r : 0), row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
       const char *src = static_cast<const char *>(a.q) +
-                        (((size_t)row * a.n_heads + h) * hd * C::kEs + (in ? c * 16 : 0));
+                        (pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) * C::kEs + (in ? c * 16 : 0));
       uint8_t *dst = q_sm + r * C::kQPitch + c * 16;
       if constexpr (TMA)
         load_query16(su32(dst), src, in);
@@ -625,8 +625,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
           }
           if (starts && ends) {
             const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
-            const int pq = q0 + n * 8 + qr, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
-            const size_t at = ((size_t)row * a.n_heads + h) * hd + d;
+            const size_t at = pairs.at(n * 8 + qr, seg.kvh, a.n_heads, hd) + d;
             if constexpr (F32)
               *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + at) = make_float2(x0 * inv, x1 * inv);
             else
@@ -716,14 +715,29 @@ __global__ void __launch_bounds__(kMergeThreads)
     const Share sh = s_share[r];
     const int qr = i - (s_end[r] - sh.nq);
     const int i0 = whole ? r + warp : r, di = whole ? W : 1;
-    // this warp's shares: r + warp, + W, ... or all of them
+    // this warp's shares: r + warp, + W, ... or all of them, kBatch at a time (their O is loaded before the weights
+    // are known)
+    constexpr int kBatch = 8;
     float M = -INFINITY, L = 0.f, acc[ND][V];
 #pragma unroll
     for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] = 0.f;
-    for (int j0 = i0; j0 <= sh.last; j0 += 32 * di) {
+    for (int j0 = i0; j0 <= sh.last; j0 += kBatch * di) {
       const int j = j0 + lane * di;
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (j <= sh.last) ml = part_ml[((size_t)j * 2 + (j == r ? sh.slot : 0)) * R + qr];
+      if (lane < kBatch && j <= sh.last) ml = part_ml[((size_t)j * 2 + (j == r ? sh.slot : 0)) * R + qr];
+      float v[kBatch][ND][V];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int jj = j0 + k * di;
+        if (jj > sh.last) break;
+        const size_t share = (size_t)jj * 2 + (jj == r ? sh.slot : 0);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const float *o = part_o + share_at(share, R, DP, qr, d * 128 + lane * V);
+          if constexpr (V == 4) *reinterpret_cast<float4 *>(v[k][d]) = *reinterpret_cast<const float4 *>(o);
+          else *reinterpret_cast<float2 *>(v[k][d]) = *reinterpret_cast<const float2 *>(o);
+        }
+      }
       const float m2 = fmaxf(M, warp_max(ml.x));
       const float f = M == -INFINITY ? 0.f : exp2f(M - m2);
       const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
@@ -731,22 +745,15 @@ __global__ void __launch_bounds__(kMergeThreads)
       M = m2;
 #pragma unroll
       for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] *= f;
-      const int n = min(32, (sh.last - j0) / di + 1);
-#pragma unroll 4
-      for (int k = 0; k < n; ++k) {
-        const int jj = j0 + k * di;
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const size_t share = (size_t)jj * 2 + (jj == r ? sh.slot : 0);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          float v[V];
-          const float *o = part_o + share_at(share, R, DP, qr, d * 128 + lane * V);
-          if constexpr (V == 4) *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
-          else *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+      for (int k = 0; k < kBatch; ++k) {
+        if (j0 + k * di > sh.last) break;
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
 #pragma unroll
           for (int e = 0; e < V; ++e)
-            if (d * 128 + lane * V + e < hd) acc[d][e] += wk * v[e];
-        }
+            if (d * 128 + lane * V + e < hd) acc[d][e] += wk * v[k][d][e];
       }
     }
     if (whole) {  // join the warps
@@ -850,9 +857,9 @@ cudaError_t paged_grid(int *grid) {
 
 cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s) {
   const int hd = a.pages.head_dim;
-  // four CTAs per SM
+  // two CTAs per SM
   auto go = [&](auto kern) {
-    return launch_pdl(kern, dim3(4 * grid), dim3(kMergeThreads), 0, s, a, kr, grid, sb.o, sb.ml, sb.desc);
+    return launch_pdl(kern, dim3(2 * grid), dim3(kMergeThreads), 0, s, a, kr, grid, sb.o, sb.ml, sb.desc);
   };
   if (a.pages.dtype == DCU_F32)
     return hd <= 64 ? go(k_paged_merge<64, float>) : hd <= 128 ? go(k_paged_merge<128, float>)

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries, OC = DP / 2;  // O columns of a half
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * kStages + 15];
+  __shared__ __align__(8) uint64_t bars[4 * kStages + 16];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_mx[2][2][2][128];  // [sub-chunk parity][tile][half] maximum of the half's keys
   __shared__ float s_l[2][2][128];      // [tile][half] share of the row sum
   __shared__ float s_m[2][128];         // [tile] final row maximum
+  __shared__ uint32_t s_bad[4];         // [chunk % 4] boxes of the chunk on bad pages
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tile A's softmax warps, per segment of two tiles whose last chunk ends inside a page: V's rows there are cleared.
   // (Tile B may be a chunk ahead or behind, so P_FULL of tile A would not do: a parity wait is only sound within one
   // phase.)
-  const uint32_t V_CLEAR = Q_FULL + 16u;
+  const uint32_t V_CLEAR = Q_FULL + 16u, A_BEGUN = Q_FULL + 24u;  // A_BEGUN: tile A has its first scores of a segment
 
   if (tid == 0) {
     // a stage is empty, and a segment final, once both tiles say so (a tile that has the chunk to itself, twice)
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; ++t) {
       mbar_init(DRAIN(t), 1);
       for (uint32_t b = 0; b < 2; ++b) {
-        mbar_init(S_FULL(t, b), 1);
+        mbar_init(S_FULL(t, b), 2);  // the scores (commit), and the issuer itself (it has seen the chunk's K_FULL)
         mbar_init(P_FULL(t, b), kSoftWarps);
       }
       mbar_init(PV_DONE(t), 1);
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(Q_FULL, 2 * kSoftWarps);
     mbar_init(O_FINAL, 2);
     mbar_init(V_CLEAR, kSoftWarps);
+    mbar_init(A_BEGUN, kSoftWarps);
     abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -143,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_enter();
   fence_proxy_async_global();  // the pages may have been written by the kernel just waited for
   tc_fence_before();
-  const Range rg = find_range<R, kKC, kWarps>(a, &s_place, s_scan, 1);  // (barriers inside)
+  Place seg;
+  const Range rg = find_range<R, kKC, kWarps>(a, seg, &s_place, s_scan, 1);  // (a barrier inside)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int *abort_v = &abort_flag;
@@ -153,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) shares[blockIdx.x].last = -1;
   } else if (warp == 0) {
     // ---- TMA producer
-    Place ld = s_place;
+    Place &ld = seg;
     const int nb = kKC / box;                     // boxes of a chunk (of each 64-dim half)
     const int my = lane % nb, half = lane / nb;   // the lane's box: lanes 0 .. nb * DP / 64 - 1 issue
     const bool mine = half < DP / 64;
@@ -169,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key = ld.blk * kKC + my * box, kvh = ld.kvh;
       const bool in = mine && key < ld.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
       if (in && !good && half == 0 && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+      const uint32_t bad = __ballot_sync(0xffffffffu, in && !good) & ((1u << nb) - 1u);  // lanes of half 0
       const int w = good ? pg : a.pages.n_pages;  // outside the tensor: zeros
       const int y = good ? key - (int)(div_page(a, (unsigned)key) * (unsigned)a.pages.page_size) : 0;
       const int c1 = head_first ? kvh : y, c2 = head_first ? y : kvh;
@@ -181,7 +185,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bounded(v ? V_EMPTY(st) : K_EMPTY(st), ph, abort_v, a.status));
         if (!ok) break;
         const uint32_t bar = v ? V_FULL(st) : K_FULL(st);
-        if (lane == 0) mbar_expect_tx(bar, C::kTile);
+        if (lane == 0) {
+          // read by the softmax once it has S of the chunk; by then tile A and B are past the entry's last use
+          if (!v) s_bad[issued & 3u] = bad;
+          mbar_expect_tx(bar, C::kTile);
+        }
         __syncwarp();
         if (mine) tma_box((v ? v_s : k_s) + st * C::kTile + dst, v ? &vmap : &kmap, half * 64, c1, c2, w, bar);
         if (v) ++issued;
@@ -222,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_mma(s_tm + h * 64u, qq + off, kd + off, id_s, kk > 0 ? 1u : 0u);
         }
         tc_commit(S_FULL(t, h));
+        mbar_arrive(S_FULL(t, h));
         if (h) {
           tc_commit(K_EMPTY(st));
           if (alone) tc_commit(K_EMPTY(st));
@@ -230,7 +239,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       any = true;
     };
-    Place seg = s_place;
     for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
       const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
       const int n = (int)(s1 - s0);
@@ -241,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j0 < n) {
         const uint32_t st = (g + j0) % kStages;
         if (!wait(K_FULL(st), (g + j0) / kStages)) break;
+        // tile B starts half a sub-chunk late, so that the two tiles' exponentials take turns
+        if (!alone && t == 1 && n > 2 && !wait(A_BEGUN, nseg)) break;
         tc_fence_after();
         issue_s(st, 0, alone);
         issue_s(st, 1, alone);
@@ -302,13 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t u = 0, g = 0, nseg = 0;  // sub-chunks of this tile, chunks of the CTA, segments
     bool alive = true;
     constexpr int kPart = kSub / 2;   // keys of a thread in a sub-chunk
-    Place seg = s_place;
     for (long long s0 = rg.u0; s0 < rg.u1; ++nseg) {
       const Seq &sq = seg.s;
       const long long s1 = min(rg.u1, s0 + (sq.nblk - seg.blk));
       const int n = (int)(s1 - s0);
       const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
       const bool alone = nq <= 128;
+      const Pairs pairs(sq, q0, G);
       const int j0 = alone ? t : 0, dj = alone ? 2 : 1;  // this tile's chunks: j0, j0 + dj, ...
       // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read
       // theirs (O_FINAL)
@@ -317,9 +327,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = st_id; i < rows * (DP / 8); i += 64 * kSoftWarps) {
           const int r = i / (DP / 8), c = i - r * (DP / 8);
           const bool in = r < nq && c * 8 < hd;
-          const int pq = q0 + (in ? r : 0), row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
           load_query16(q_s + (uint32_t)(r >> 7) * C::kTile + tile_off(r & 127, c),
-                       static_cast<const bf16 *>(a.q) + ((size_t)row * a.n_heads + h) * hd + (in ? c * 8 : 0), in);
+                       static_cast<const bf16 *>(a.q) + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0),
+                       in);
         }
         load_query_wait();
         fence_proxy_async_smem();
@@ -327,32 +337,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(Q_FULL);
       }
       float m_run = -INFINITY, l_run = 0.f;
-      // the pages of this thread's keys of a sub-chunk (two boxes of 16 slots at most), looked up one ahead
-      auto look = [&](int key) {
-        key += pt * kPart + lane * box;
-        return lane < 2 && lane * box < kPart && key < sq.nk
-                   ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)]
-                   : 0;
-      };
       const int ns = j0 < n ? 2 * ((n - j0 + dj - 1) / dj) : 0;  // this tile's sub-chunks
-      int pg = ns ? look((seg.blk + j0) * kKC) : 0;
+      const bool used = (alone ? 0 : t * 128) + q4 * 32 < nq;     // this warp has queries
       for (int i = 0; i < ns; ++i, ++u) {
         const int j = j0 + (i >> 1) * dj, key0 = (seg.blk + j) * kKC + (i & 1) * kSub;
         const uint32_t hb = (uint32_t)(i & 1), s_buf = s_tm + hb * 64u;
-        const uint32_t bad = __ballot_sync(0xffffffffu, pg < 0 || pg >= a.pages.n_pages);
-        if (i + 1 < ns) pg = look((seg.blk + j0 + ((i + 1) >> 1) * dj) * kKC + ((i + 1) & 1) * kSub);
         if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(t, hb), (u >> 1) & 1u, abort_v, a.status));
         const int nv = sq.nk - key0 - pt * kPart;  // valid keys of this thread
+        const uint32_t gj = g + (uint32_t)j;
+        if (t == 0 && i == 0 && lane == 0) mbar_arrive(A_BEGUN);
+        if (used) {
         uint32_t sr[kPart];  // raw scores: the scale (> 0) commutes with the maximum and enters the exponent
         float mc = -INFINITY;
         if (alive) {
           tc_fence_after();
           tmem_ld32_issue(s_buf + (uint32_t)(pt * kPart), sr);
           tmem_wait_ld_tie32(sr);
+          const uint32_t bad = s_bad[gj & 3u];
           if (nv < kPart || bad) {
             uint32_t valid = nv >= kPart ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
-            if (bad & 1u) valid &= box >= kPart ? 0u : ~0u << box;
-            if (bad & 2u) valid &= (1u << box) - 1u;
+            const int k0 = (i & 1) * kSub + pt * kPart;  // this thread's keys in the chunk: one box, or two of 16
+            if ((bad >> (k0 / box)) & 1u) valid &= box >= kPart ? 0u : ~0u << box;
+            if (box < kPart && ((bad >> (k0 / box + 1)) & 1u)) valid &= (1u << box) - 1u;
 #pragma unroll
             for (int c = 0; c < kPart; ++c)
               if (!((valid >> c) & 1u)) sr[c] = 0xff800000u;  // -inf
@@ -399,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P: 16 columns over the upper half of this thread's own scores
         tmem_st16u(s_buf + (uint32_t)(pt * kPart + 16), sr);
         l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        }
         if (hb == 0 && (alone || t == 0) && sq.nk - key0 < kKC) {
           // past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
           // zeros; the rows are cleared after the copy and before P_FULL lets P V start.
-          const uint32_t gj = g + (uint32_t)j;
           alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(gj % kStages), (gj / kStages) & 1u, abort_v, a.status));
           if (!alive) continue;
           const int r0 = max(sq.nk - key0, 0), r1 = min(kKC, (r0 + box - 1) / box * box);
@@ -449,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (alive) {
         tc_fence_after();
-        const int pq = q0 + q, row = sq.row0 + pq / G, h = seg.kvh * G + pq % G;
-        bf16 *dst = static_cast<bf16 *>(a.out) + ((size_t)row * a.n_heads + h) * hd;
+        bf16 *dst = static_cast<bf16 *>(a.out) + pairs.at(q < nq ? q : 0, seg.kvh, a.n_heads, hd);
+        float *po = part_o + share_at(share, R, DP, q, 0);
         const float inv = starts && ends ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
         const uint32_t oa = tmem + C::kO + (alone ? 0u : 128u * t) + lane_off;
 #pragma unroll 1
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                *reinterpret_cast<float4 *>(part_o + share_at(share, R, DP, q, c + 4 * e)) =
+                *reinterpret_cast<float4 *>(po + (c / 4 + e) * (R * 4)) =
                     make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
             }
           }

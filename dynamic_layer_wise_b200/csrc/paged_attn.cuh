@@ -101,12 +101,58 @@ __device__ __forceinline__ long long div_ll(long long a, int b) {
   return a < (1ll << 32) ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// All W warps of the CTA: the CTA's range, its first place in *place (shared
-// memory; valid for every thread on return).  A launch uses as many ranges as
-// have at least `least` units each (the grid at most).
+// Cuts `total` units for the CTA; kept out of line of the place search so that
+// one sequence (B == 1) needs neither the scan nor a barrier.
+__device__ __forceinline__ void cut_even(Range &rg, long long total, int ranges) {
+  const int bid = (int)blockIdx.x;
+  rg.parts = 0;
+  rg.any = bid < ranges;
+  rg.q = ranges ? div_ll(total, ranges) : 0;
+  rg.rem = (int)(total - rg.q * ranges);
+  rg.u0 = bid * rg.q + min(bid, rg.rem);
+  rg.u1 = rg.u0 + rg.q + (bid < rg.rem ? 1 : 0);
+}
+// Item, kv head, tile and block of unit `off` of sequence p.s.
+__device__ __forceinline__ void locate(Place &p, long long off) {
+  const long long item = div_ll(off, p.s.nblk);
+  p.blk = (int)(off - item * p.s.nblk);
+  p.kvh = (int)div_ll(item, p.s.tiles);
+  p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
+}
+
+// All W warps of the CTA: its range, and its first place in `first`.  A launch
+// uses as many ranges as have at least `least` units each (the grid at most).
 template <int R, int KB, int W>
-__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place, long long *scan, int least) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, KV = a.pages.n_kv_heads;
+__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first, Place *place, long long *scan,
+                                            int least) {
+  const int KV = a.pages.n_kv_heads;
+  Range rg;
+  if (a.B == 1) {
+    Place p;
+    p.b = 0;
+    p.s = seq_of<R, KB>(a, 0);
+    const long long total = p.s.units(KV);
+    const int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
+    cut_even(rg, total, ranges);
+    const long long items = (long long)KV * p.s.tiles;
+    if (total > 0 && items <= ranges) {
+      // cut item by item when that adds no more to the longest range than `least` units, which a second item would cost
+      const int f = ranges / (int)items;
+      if ((p.s.nblk + f - 1) / f <= (int)rg.q + (rg.rem ? 1 : 0) + least) {
+        const int item = (int)blockIdx.x / f, part = (int)blockIdx.x - item * f;
+        rg.parts = f;
+        rg.any = item < items;
+        rg.q = p.s.nblk;
+        rg.u0 = (long long)item * p.s.nblk + div_ll((long long)part * p.s.nblk, f);
+        rg.u1 = (long long)item * p.s.nblk + div_ll((long long)(part + 1) * p.s.nblk, f);
+      }
+    }
+    if (rg.any) locate(p, rg.u0);
+    first = p;
+    __syncthreads();  // (the callers' shared state is set up by one thread)
+    return rg;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + 32 * W - 1) / (32 * W);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
@@ -124,41 +170,13 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
   }
   if (lane == 31) scan[warp] = x;
   __syncthreads();
-  Range rg;
   long long base = 0, total = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     if (i == warp) base = total;
     total += scan[i];
   }
-  int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
-  const int bid = (int)blockIdx.x;
-  rg.parts = 0;
-  if (a.B == 1 && total > 0) {
-    // cut item by item when that adds no more to the longest range than `least` units, which a second item would cost
-    const Seq s = seq_of<R, KB>(a, 0);
-    const long long items = (long long)KV * s.tiles;
-    if (items <= ranges) {
-      const int f = ranges / (int)items;
-      if ((s.nblk + f - 1) / f <= (int)div_ll(total + ranges - 1, ranges) + least) {
-        rg.parts = f;
-        ranges = (int)items * f;
-        rg.any = bid < ranges;
-        rg.q = s.nblk;
-        rg.rem = 0;
-        const int item = bid / f, part = bid - item * f;
-        rg.u0 = (long long)item * s.nblk + div_ll((long long)part * s.nblk, f);
-        rg.u1 = (long long)item * s.nblk + div_ll((long long)(part + 1) * s.nblk, f);
-      }
-    }
-  }
-  if (!rg.parts) {
-    rg.any = bid < ranges;
-    rg.q = ranges ? div_ll(total, ranges) : 0;
-    rg.rem = (int)(total - rg.q * ranges);
-    rg.u0 = bid * rg.q + min(bid, rg.rem);
-    rg.u1 = rg.u0 + rg.q + (bid < rg.rem ? 1 : 0);
-  }
+  cut_even(rg, total, (int)min((long long)gridDim.x, div_ll(total + least - 1, least)));
   long long at = base + x - mine;
   if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
     if (per > 1)
@@ -167,15 +185,31 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place *place
         if (rg.u0 < at + p.s.units(KV)) break;
         at += p.s.units(KV);
       }
-    const long long off = rg.u0 - at, item = div_ll(off, p.s.nblk);
-    p.blk = (int)(off - item * p.s.nblk);
-    p.kvh = (int)div_ll(item, p.s.tiles);
-    p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
+    locate(p, rg.u0 - at);
     *place = p;
   }
   __syncthreads();
+  first = *place;
   return rg;
 }
+
+// The (row, head) pairs of a tile: query r is row r0 + (h0 + r) / G, head h0 + r
+// modulo G of the group.
+struct Pairs {
+  int row0, h0, G;
+  float inv;
+  __device__ __forceinline__ Pairs(const Seq &s, int q0, int G_) : G(G_), inv(1.f / (float)G_) {
+    row0 = s.row0 + q0 / G;
+    h0 = q0 % G;
+  }
+  // element offset of query r (< 256) of kv head kvh in [rows][H][hd]; exact: h0 + r is far below 2^21, where the
+  // fp32 product's error stays below the distance 0.5 / G to the next integer
+  __device__ __forceinline__ size_t at(int r, int kvh, int H, int hd) const {
+    const int i = h0 + r;
+    const int d = G == 1 ? i : (int)(((float)i + 0.5f) * inv);
+    return ((size_t)(row0 + d) * H + kvh * G + (i - d * G)) * hd;
+  }
+};
 
 // Place of dim d of query q in a share of kr queries: groups of 4 dims, so the
 // threads that write a share (one query each) store whole lines.
