@@ -799,27 +799,24 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 template <int DP, bool F32, int NT, bool TMA>
-cudaError_t launch_variant(const PagedAttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int head_first,
-                           void *ws, cudaStream_t s) {
+cudaError_t launch_variant(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s) {
   using C = Cfg<DP, F32, NT>;
   static std::atomic<uint64_t> attr{0};
   if (cudaError_t e = ensure_smem_limit(k_paged_attn<DP, F32, NT, TMA>, C::kSmem, attr)) return e;
   int grid = 0;
   if (cudaError_t e = paged_grid(&grid)) return e;
   const ShareBuf sb(ws, C::kR, DP);
-  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, kmap,
-                                 vmap, head_first, sb.o, sb.ml, sb.desc))
+  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, m.k,
+                                 m.v, m.head_first, sb.o, sb.ml, sb.desc))
     return e;
   return launch_paged_merge(a, C::kR, grid, sb, s);
 }
 
 template <int DP, bool F32, int NT>
 cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
-  CUtensorMap kmap = {}, vmap = {};
-  int head_first = 0;
-  if (page_maps(a.pages, Cfg<DP, F32, NT>::kKB, &kmap, &vmap, &head_first))
-    return launch_variant<DP, F32, NT, true>(a, kmap, vmap, head_first, ws, s);
-  return launch_variant<DP, F32, NT, false>(a, kmap, vmap, head_first, ws, s);
+  PageMaps m = {};
+  if (page_maps(a.pages, Cfg<DP, F32, NT>::kKB, &m)) return launch_variant<DP, F32, NT, true>(a, m, ws, s);
+  return launch_variant<DP, F32, NT, false>(a, m, ws, s);
 }
 
 }  // namespace
@@ -828,7 +825,7 @@ cudaError_t launch(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
 // bytes x kb slots.  false, and the kernel loads key by key with cp.async,
 // where a block of kb keys could cross a page or the strides do not nest (each
 // a multiple of the one below and past its extent, as a tensor map wants).
-bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap, int *head_first) {
+bool page_maps(const dcu_pages &p, int kb, PageMaps *m) {
   if (p.page_size % kb) return false;
   const bool f32 = p.dtype == DCU_F32;
   const uint64_t es = f32 ? 4 : 2, row = (uint64_t)p.head_dim * es;
@@ -843,8 +840,9 @@ bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap,
   const uint64_t dims[4] = {(uint64_t)p.head_dim, n0, n1, (uint64_t)p.n_pages};
   const uint64_t st[3] = {s0, s1, s2};
   const uint32_t box[4] = {(uint32_t)(128 / es), hf ? 1u : (uint32_t)kb, hf ? (uint32_t)kb : 1u, 1u};
-  *head_first = hf;
-  return encode_tmap_4d(kmap, f32, p.k, dims, st, box) && encode_tmap_4d(vmap, f32, p.v, dims, st, box);
+  m->box = kb;
+  m->head_first = hf;
+  return encode_tmap_4d(&m->k, f32, p.k, dims, st, box) && encode_tmap_4d(&m->v, f32, p.v, dims, st, box);
 }
 
 cudaError_t paged_grid(int *grid) {
@@ -868,6 +866,10 @@ cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const S
                                                             : go(k_paged_merge<256, bf16>);
 }
 
+// Queries per sequence and kv head, on average, above which the tcgen05 kernel
+// is taken.
+constexpr long long kTcMinQueries = 32;
+
 int64_t paged_attention_workspace(const dcu_pages &p) {
   const int dp = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
   if (p.dtype == DCU_F32) return ShareBuf::bytes(8, dp);
@@ -884,7 +886,10 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
   if (queries <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
-  if (queries > 32ll * a.B && a.scale_log2 > 0.f && tc_box_keys(a.pages)) return launch_paged_attention_tc(a, ws, s);
+  PageMaps m;
+  if (queries > kTcMinQueries * a.B && a.scale_log2 > 0.f && hd <= 128 && a.pages.page_size % 16 == 0 &&
+      page_maps(a.pages, tc_box_keys(a.pages), &m))
+    return launch_paged_attention_tc(a, m, ws, s);
   return hd <= 64 ? launch<64, false, 4>(a, ws, s)
                   : hd <= 128 ? launch<128, false, 4>(a, ws, s) : launch<256, false, 2>(a, ws, s);
 }

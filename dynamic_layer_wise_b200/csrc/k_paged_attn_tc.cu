@@ -512,18 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DP>
-cudaError_t launch_dp(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
+cudaError_t launch_dp(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s) {
   using C = TcCfg<DP>;
   static std::atomic<uint64_t> attr{0};
   if (cudaError_t e = ensure_smem_limit(k_paged_attn_tc<DP>, (int)C::kSmem, attr)) return e;
-  CUtensorMap kmap, vmap;
-  int head_first = 0, grid = 0;
-  const int box = tc_box_keys(a.pages);
-  if (!box || !page_maps(a.pages, box, &kmap, &vmap, &head_first)) return cudaErrorInvalidValue;
+  int grid = 0;
   if (cudaError_t e = paged_grid(&grid)) return e;
   const ShareBuf sb(ws, kTcQueries, DP);
-  if (cudaError_t e = launch_pdl(k_paged_attn_tc<DP>, dim3(grid), dim3(kThreads), C::kSmem, s, a, kmap, vmap,
-                                 head_first, box, sb.o, sb.ml, sb.desc))
+  if (cudaError_t e = launch_pdl(k_paged_attn_tc<DP>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m.k, m.v,
+                                 m.head_first, m.box, sb.o, sb.ml, sb.desc))
     return e;
   return launch_paged_merge(a, kTcQueries, grid, sb, s);
 }
@@ -531,16 +528,13 @@ cudaError_t launch_dp(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
 }  // namespace
 
 int tc_box_keys(const dcu_pages &p) {
-  CUtensorMap k, v;
-  int hf = 0;
-  if (p.dtype != DCU_BF16 || p.head_dim > 128) return 0;
   int box = 16;
   while (box < 128 && p.page_size % (2 * box) == 0) box *= 2;
-  return page_maps(p, box, &k, &v, &hf) ? box : 0;
+  return box;
 }
 
-cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
-  return a.pages.head_dim <= 64 ? launch_dp<64>(a, ws, s) : launch_dp<128>(a, ws, s);
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s) {
+  return a.pages.head_dim <= 64 ? launch_dp<64>(a, m, ws, s) : launch_dp<128>(a, m, ws, s);
 }
 
 }  // namespace dcu

@@ -236,14 +236,20 @@ struct ShareBuf {
   }
 };
 
+// Tensor maps of a layer's pages: box of kb slots, dims (d, head, slot, page)
+// when head_first, else (d, slot, head, page).
+struct PageMaps {
+  CUtensorMap k, v;
+  int box, head_first;
+};
 // k_paged_attn.cu
-bool page_maps(const dcu_pages &p, int kb, CUtensorMap *kmap, CUtensorMap *vmap, int *head_first);
+bool page_maps(const dcu_pages &p, int kb, PageMaps *m);
 cudaError_t paged_grid(int *grid);  // one range per SM
 cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s);
 
 // k_paged_attn_tc.cu: bf16, head_dim <= 128, boxes of box_keys (16 .. 128) slots of one page
 constexpr int kTcQueries = 256;  // queries of a tile
-int tc_box_keys(const dcu_pages &p);  // 0: the pages do not suit
-cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, void *ws, cudaStream_t s);
+int tc_box_keys(const dcu_pages &p);  // slots of a box (page_size % 16 == 0)
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s);
 
 }  // namespace dcu

@@ -396,32 +396,32 @@ _current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _run(device, stream, call):
-    """call(raw stream) with `device` and `stream` (None: the device's current stream) current."""
+def _run(device, stream, call, args):
+    """call(raw stream, *args) with `device` and `stream` (None: the device's current stream) current."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got tensors on {device}")
+    if stream is None and device.index == torch.cuda.current_device():
+        return call(_current_raw(device.index), *args)
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(_current_raw(device.index))
         with torch.cuda.device(device):
-            return call(_current_raw(device.index))
+            return call(_current_raw(device.index), *args)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
             torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"stream of {stream.device} for tensors of {device}")
     with torch.cuda.stream(stream):
-        return call(stream.cuda_stream)
+        return call(stream.cuda_stream, *args)
 
 
 def _arg(t, name: str, dtype, shape, device):
-    """Address of a contiguous CUDA tensor of `dtype`, `shape` and `device`."""
-    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda
-            and t.is_contiguous()):
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                     f"{device if device.type == 'cuda' else 'a CUDA device'}, got {t.dtype} {tuple(t.shape)} with "
-                     f"strides {t.stride()} on {t.device}")
+    """Address of a contiguous tensor of `dtype`, `shape` and `device`."""
+    if isinstance(t, torch.Tensor):
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    raise TypeError(f"{name}: expected a torch.Tensor")
 
 
 def _opt(t, name: str, dtype, shape, device):
@@ -461,20 +461,21 @@ def dcu_page_table(lens, page_size: int, max_pages: int, n_pages: int, pool=None
     B, = _dims(lens, "lens", 1)
     dev = lens.device
     n_pool = n_pages if pool is None else _dims(pool, "pool", 1)[0]
-    args = (_arg(lens, "lens", _I32, (B,), dev), B, page_size, max_pages, n_pages,
-            _opt(pool, "pool", _I32, (n_pool,), dev), n_pool, _opt(first, "first", _I32, (1,), dev))
-    p_status = _opt(status, "status", _I32, (1,), dev)
     if max_pages <= 0:
         raise ValueError("max_pages must be positive")
+    return _run(dev, stream, _page_table, (
+        lens, _arg(lens, "lens", _I32, (B,), dev), B, page_size, max_pages, n_pages,
+        _opt(pool, "pool", _I32, (n_pool,), dev), n_pool, _opt(first, "first", _I32, (1,), dev),
+        _opt(status, "status", _I32, (1,), dev)))
 
-    def call(raw):
-        table = torch.empty(B, max_pages, dtype=_I32, device=dev)
-        held = torch.empty(B, dtype=_I32, device=dev)
-        nxt = torch.empty(1, dtype=_I32, device=dev)
-        _check(lib().dcu_page_table(*args, table.data_ptr(), held.data_ptr(), nxt.data_ptr(), p_status, raw))
-        return table, held, nxt
 
-    return _run(dev, stream, call)
+def _page_table(raw, lens, p_lens, B, page_size, max_pages, n_pages, p_pool, n_pool, p_first, p_status):
+    table = torch.empty(B, max_pages, dtype=_I32, device=lens.device)
+    held = torch.empty_like(lens)
+    nxt = torch.empty(1, dtype=_I32, device=lens.device)
+    _check(lib().dcu_page_table(p_lens, B, page_size, max_pages, n_pages, p_pool, n_pool, p_first, table.data_ptr(),
+                                held.data_ptr(), nxt.data_ptr(), p_status, raw))
+    return table, held, nxt
 
 
 def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=None, first=None, status=None,
@@ -485,21 +486,21 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
     B, max_pages = _dims(table, "table", 2)
     dev = table.device
     N = 0 if pos is None else _dims(pos, "pos", 2)[1]
-    args = (_arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
-            _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
-            _opt(first, "first", _I32, (B,), dev), max_rows)
-    p_status = _opt(status, "status", _I32, (1,), dev)
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
+    return _run(dev, stream, _slot_map, (
+        dev, _arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
+        _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
+        _opt(first, "first", _I32, (B,), dev), max_rows, _opt(status, "status", _I32, (1,), dev)))
 
-    def call(raw):
-        row_start = torch.empty(B + 1, dtype=_I32, device=dev)
-        row_pos = torch.empty(max_rows, dtype=_I32, device=dev)
-        slot = torch.empty(max_rows, dtype=_I32, device=dev)
-        _check(lib().dcu_slot_map(*args, row_start.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), p_status, raw))
-        return row_start, row_pos, slot
 
-    return _run(dev, stream, call)
+def _slot_map(raw, dev, p_table, B, max_pages, page_size, n_pages, p_count, p_pos, N, p_first, max_rows, p_status):
+    row_start = torch.empty(B + 1, dtype=_I32, device=dev)
+    row_pos = torch.empty(max_rows, dtype=_I32, device=dev)
+    slot = torch.empty_like(row_pos)
+    _check(lib().dcu_slot_map(p_table, B, max_pages, page_size, n_pages, p_count, p_pos, N, p_first, max_rows,
+                              row_start.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), p_status, raw))
+    return row_start, row_pos, slot
 
 
 def dcu_rope_table(max_pos: int, head_dim: int, theta: float = 10000.0, device="cuda", stream=None):
@@ -517,7 +518,7 @@ def dcu_rope_table(max_pos: int, head_dim: int, theta: float = 10000.0, device="
         _check(lib().dcu_rope_table(tab.data_ptr(), max_pos, head_dim, theta, raw))
         return tab
 
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, ())
 
 
 def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_heads: int, q=None, status=None,
@@ -536,20 +537,22 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
     if n_start < 1:
         raise ValueError("row_start: expected at least one entry")
     max_pos = 0 if rope is None else _dims(rope, "rope", 3)[0]
-    args = (_arg(qkv, "qkv", torch.float32, (T, width), dev), T,
-            _arg(row_start, "row_start", _I32, (n_start,), dev) + 4 * (n_start - 1),
-            _arg(row_pos, "row_pos", _I32, (T,), dev), _arg(slot, "slot", _I32, (T,), dev),
-            _opt(rope, "rope", torch.float32, (max_pos, hd // 2, 2), dev), max_pos, n_heads, pages)
-    p_status = _opt(status, "status", _I32, (1,), dev)
     if q is not None:
         _arg(q, "q", k_pages.dtype, (T, n_heads, hd), dev)
+    return _run(dev, stream, _paged_write, (
+        k_pages, q, _arg(qkv, "qkv", torch.float32, (T, width), dev), T,
+        _arg(row_start, "row_start", _I32, (n_start,), dev) + 4 * (n_start - 1),
+        _arg(row_pos, "row_pos", _I32, (T,), dev), _arg(slot, "slot", _I32, (T,), dev),
+        _opt(rope, "rope", torch.float32, (max_pos, hd // 2, 2), dev), max_pos, n_heads, pages,
+        _opt(status, "status", _I32, (1,), dev)))
 
-    def call(raw):
-        out = torch.empty(T, n_heads, hd, dtype=k_pages.dtype, device=dev) if q is None else q
-        _check(lib().dcu_paged_write(*args, out.data_ptr(), p_status, raw))
-        return out
 
-    return _run(dev, stream, call)
+def _paged_write(raw, k_pages, q, p_qkv, T, p_rows, p_pos, p_slot, p_rope, max_pos, n_heads, pages, p_status):
+    if q is None:
+        q = torch.empty(T, n_heads, pages.head_dim, dtype=k_pages.dtype, device=k_pages.device)
+    _check(lib().dcu_paged_write(p_qkv, T, p_rows, p_pos, p_slot, p_rope, max_pos, n_heads, pages, q.data_ptr(),
+                                 p_status, raw))
+    return q
 
 
 def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: float | None = None, out=None,
@@ -563,23 +566,25 @@ def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: fl
     dev = q.device
     pages = _pages(k_pages, v_pages, dev)
     B, max_pages = _dims(table, "table", 2)
-    p_q = _arg(q, "q", k_pages.dtype, (T, H, pages.head_dim), dev)
-    args = (p_q, T, _arg(row_start, "row_start", _I32, (B + 1,), dev), B, _arg(kv_len, "kv_len", _I32, (B,), dev),
-            _arg(table, "table", _I32, (B, max_pages), dev), max_pages, H, pages,
-            hd ** -0.5 if scale is None else scale)
-    p_status = _opt(status, "status", _I32, (1,), dev)
     if out is not None:
         _arg(out, "out", q.dtype, (T, H, hd), dev)
     if workspace is not None:
         _arg(workspace, "workspace", torch.uint8, (_dims(workspace, "workspace", 1)[0],), dev)
+    return _run(dev, stream, _paged_attention, (
+        q, out, workspace, _arg(q, "q", k_pages.dtype, (T, H, pages.head_dim), dev), T,
+        _arg(row_start, "row_start", _I32, (B + 1,), dev), B, _arg(kv_len, "kv_len", _I32, (B,), dev),
+        _arg(table, "table", _I32, (B, max_pages), dev), max_pages, H, pages, hd ** -0.5 if scale is None else scale,
+        _opt(status, "status", _I32, (1,), dev)))
 
-    def call(raw):
-        o = torch.empty_like(q) if out is None else out
-        ws = torch.empty(_workspace_bytes(pages), dtype=torch.uint8, device=dev) if workspace is None else workspace
-        _check(lib().dcu_paged_attention(*args, o.data_ptr(), ws.data_ptr(), ws.numel(), p_status, raw))
-        return o
 
-    return _run(dev, stream, call)
+def _paged_attention(raw, q, out, workspace, p_q, T, p_start, B, p_len, p_table, max_pages, H, pages, scale, p_status):
+    if out is None:
+        out = torch.empty_like(q)
+    if workspace is None:
+        workspace = torch.empty(_workspace_bytes(pages), dtype=torch.uint8, device=q.device)
+    _check(lib().dcu_paged_attention(p_q, T, p_start, B, p_len, p_table, max_pages, H, pages, scale, out.data_ptr(),
+                                     workspace.data_ptr(), workspace.numel(), p_status, raw))
+    return out
 
 
 def _workspace_bytes(pages: dcu_pages) -> int:

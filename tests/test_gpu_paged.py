@@ -140,12 +140,14 @@ def test_slot_map_bad_rows():
     assert sl.cpu().tolist() == [-1, -1, -1, -1, 3 * 16 + 15, -1] and st.item() == R.BAD_PAGE
 
 
-def test_slot_map_leaves_rows_behind_the_last_sequence(monkeypatch):
-    keep = torch.empty
-    monkeypatch.setattr(torch, "empty", lambda *a, **k: keep(*a, **k).fill_(-77))
+def test_slot_map_leaves_rows_behind_the_last_sequence():
     table, n_pages = make_table(np.random.default_rng(0), [40, 40], 16)
-    start, rp, sl = dcu.dcu_slot_map(i32(table), i32([3, 4]), 16, n_pages, 600)
-    assert start.cpu().tolist() == [0, 3, 7]
+    t, c = i32(table), i32([3, 4])
+    start, rp, sl = (torch.full((n,), -77, dtype=torch.int32, device="cuda") for n in (3, 600, 600))
+    rc = dcu.lib().dcu_slot_map(t.data_ptr(), 2, table.shape[1], 16, n_pages, c.data_ptr(), None, 0, None, 600,
+                                start.data_ptr(), rp.data_ptr(), sl.data_ptr(), None,
+                                torch.cuda.current_stream().cuda_stream)
+    assert rc == dcu.DCU_OK and start.cpu().tolist() == [0, 3, 7]
     assert (rp[7:] == -77).all() and (sl[7:] == -77).all() and (sl[:7] >= 0).all()
 
 
