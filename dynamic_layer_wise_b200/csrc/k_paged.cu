@@ -48,6 +48,7 @@ __device__ __forceinline__ long long pages_needed(int len, int page_size, int ma
 
 constexpr int kTabThreads = 256;
 constexpr int kTabCols = 4096;
+constexpr int kTabBatch = 4;
 
 __global__ void __launch_bounds__(kTabThreads)
     k_page_table(const int32_t *__restrict__ lens, int B, int page_size, int max_pages, int n_pages,
@@ -86,20 +87,28 @@ __global__ void __launch_bounds__(kTabThreads)
     }
   }
   __syncthreads();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int r = w; r < nr; r += kTabThreads / 32) {
-    int32_t *row = table + (size_t)(b0 + r) * max_pages;
-    const int h = s_held[r], src = s_src[r];
-    for (int c = c0 + lane; c < c1; c += 32) {
-      int pg = -1;
-      if (c < h) {
-        pg = pool ? pool[src + c] : src + c;
-        if (pg < 0 || pg >= n_pages) {
-          pg = -1;
+  // columns dealt out to the threads, kTabBatch pool loads of a thread in flight
+  const int nc = c1 - c0;
+  for (int r = 0; r < nr; ++r) {
+    int32_t *row = table + (size_t)(b0 + r) * max_pages + c0;
+    const int h = s_held[r] - c0, src = s_src[r] + c0;
+    for (int c = threadIdx.x; c < nc; c += kTabThreads * kTabBatch) {
+      int pg[kTabBatch];
+#pragma unroll
+      for (int e = 0; e < kTabBatch; ++e) {
+        const int k = c + e * kTabThreads;
+        pg[e] = k < h ? (pool ? pool[src + k] : src + k) : -1;
+      }
+#pragma unroll
+      for (int e = 0; e < kTabBatch; ++e) {
+        const int k = c + e * kTabThreads;
+        if (k >= nc) break;
+        if (k < h && (pg[e] < 0 || pg[e] >= n_pages)) {
+          pg[e] = -1;
           flag(status, DCU_ST_BAD_PAGE);
         }
+        row[k] = pg[e];
       }
-      row[c] = pg;
     }
   }
 }
@@ -203,11 +212,12 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
   reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-constexpr int kWriteThreads = 256;
-constexpr int kWriteItems = 2;  // items per thread
+// grid (rows, slices of a row): each thread has one item of one row, and its 64
+// bytes are on the way before the row's slot and position are known.
+constexpr int kWriteMax = 512;  // most threads of a CTA
 
 template <class T>
-__global__ void __launch_bounds__(kWriteThreads)
+__global__ void __launch_bounds__(kWriteMax)
     k_paged_write(const float *__restrict__ qkv, int max_rows, const int32_t *__restrict__ n_rows,
                   const int32_t *__restrict__ row_pos, const int32_t *__restrict__ slot,
                   const float2 *__restrict__ rope, int max_pos, int H, const dcu_pages pg, T *__restrict__ q,
@@ -215,57 +225,49 @@ __global__ void __launch_bounds__(kWriteThreads)
   pdl_enter();
   const int hd = pg.head_dim, KV = pg.n_kv_heads, half = hd / 2;
   const int n_rope = (H + KV) * (half / 8), items = n_rope + KV * (hd / 16);
-  const int rows = n_rows ? min(*n_rows, max_rows) : max_rows;
+  const int t = blockIdx.x, u = blockIdx.y * blockDim.x + threadIdx.x;
+  if (u >= items) return;
+  // element offsets of the item's two vectors of 8 in the row
+  const bool is_v = u >= n_rope;
+  const int per = is_v ? hd / 16 : half / 8, head = (is_v ? u - n_rope : u) / per;
+  const int j = ((is_v ? u - n_rope : u) - head * per) * (is_v ? 16 : 8);
+  const int second = is_v ? 8 : half;
+  const float *x = qkv + (size_t)t * (size_t)(H + 2 * KV) * hd + (size_t)(is_v ? H + KV + head : head) * hd + j;
+  float a[8], b[8];
+  load8(x, a);
+  load8(x + second, b);
+  const int sl = slot[t], p = rope ? row_pos[t] : 0, used = n_rows ? *n_rows : max_rows;
+  if (t >= used) return;
   const long long n_slots = (long long)pg.n_pages * pg.page_size;
-  for (int t = blockIdx.x; t < rows; t += gridDim.x) {
-    const int sl = slot[t], p = rope ? row_pos[t] : 0;
-    const bool good = !rope || (p >= 0 && p < max_pos);
-    const bool keep = good && sl >= 0 && sl < n_slots;
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
-      if (!good) flag(status, DCU_ST_BAD_ROW);
-      if (sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
-    }
-    const float *x = qkv + (size_t)t * (size_t)(H + 2 * KV) * hd;
-    const int page = keep ? sl / pg.page_size : 0;
-    const int64_t at = (int64_t)page * pg.page_stride + (int64_t)(keep ? sl - page * pg.page_size : 0) * pg.slot_stride;
-    for (int u = blockIdx.y * kWriteThreads + threadIdx.x; u < items; u += gridDim.y * kWriteThreads) {
-      float a[8], b[8];
-      if (u < n_rope) {
-        const int head = u / (half / 8), j = (u - head * (half / 8)) * 8;
-        T *dst;
-        if (head < H) {
-          dst = q + ((size_t)t * H + head) * hd + j;
-        } else {
-          if (!keep) continue;
-          dst = static_cast<T *>(pg.k) + at + (int64_t)(head - H) * pg.head_stride + j;
-        }
-        load8(x + (size_t)head * hd + j, a);
-        load8(x + (size_t)head * hd + j + half, b);
-        if (rope) {
-          const float4 *cs = reinterpret_cast<const float4 *>(rope + (size_t)(good ? p : 0) * half + j);
+  const bool good = !rope || (p >= 0 && p < max_pos);
+  if (u == 0) {
+    if (!good) flag(status, DCU_ST_BAD_ROW);
+    if (sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
+  }
+  T *dst;
+  if (!is_v && head < H) {
+    dst = q + ((size_t)t * H + head) * hd + j;
+  } else {
+    if (!good || sl < 0 || sl >= n_slots) return;
+    const int page = (int)((unsigned)sl / (unsigned)pg.page_size);
+    dst = static_cast<T *>(is_v ? pg.v : pg.k) + (int64_t)page * pg.page_stride +
+          (int64_t)(sl - page * pg.page_size) * pg.slot_stride + (int64_t)(is_v ? head : head - H) * pg.head_stride + j;
+  }
+  if (rope && !is_v) {
+    const float4 *cs = reinterpret_cast<const float4 *>(rope + (size_t)(good ? p : 0) * half + j);
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float4 c = __ldg(cs + e / 2);
-            const float a0 = a[e] * c.x - b[e] * c.y, b0 = b[e] * c.x + a[e] * c.y;
-            const float a1 = a[e + 1] * c.z - b[e + 1] * c.w, b1 = b[e + 1] * c.z + a[e + 1] * c.w;
-            a[e] = good ? a0 : 0.f;
-            b[e] = good ? b0 : 0.f;
-            a[e + 1] = good ? a1 : 0.f;
-            b[e + 1] = good ? b1 : 0.f;
-          }
-        }
-        store8(dst, a);
-        store8(dst + half, b);
-      } else if (keep) {
-        const int v = u - n_rope, head = v / (hd / 16), j = (v - head * (hd / 16)) * 16;
-        T *dst = static_cast<T *>(pg.v) + at + (int64_t)head * pg.head_stride + j;
-        load8(x + (size_t)(H + KV + head) * hd + j, a);
-        load8(x + (size_t)(H + KV + head) * hd + j + 8, b);
-        store8(dst, a);
-        store8(dst + 8, b);
-      }
+    for (int e = 0; e < 8; e += 2) {
+      const float4 c = __ldg(cs + e / 2);
+      const float a0 = a[e] * c.x - b[e] * c.y, b0 = b[e] * c.x + a[e] * c.y;
+      const float a1 = a[e + 1] * c.z - b[e + 1] * c.w, b1 = b[e + 1] * c.z + a[e + 1] * c.w;
+      a[e] = good ? a0 : 0.f;
+      b[e] = good ? b0 : 0.f;
+      a[e + 1] = good ? a1 : 0.f;
+      b[e + 1] = good ? b1 : 0.f;
     }
   }
+  store8(dst, a);
+  store8(dst + second, b);
 }
 
 }  // namespace
@@ -278,9 +280,8 @@ cudaError_t launch_page_table(const int32_t *lens, int B, int page_size, int max
   if (per > kTabThreads) per = kTabThreads;
   const dim3 grid((B + per - 1) / per, (max_pages + kTabCols - 1) / kTabCols);
   if (grid.y > 65535) return cudaErrorInvalidValue;
-  launch_pdl(k_page_table, grid, dim3(kTabThreads), 0, s, lens, B, page_size, max_pages, n_pages, pool, n_pool, first,
-             per, table, held, next, status);
-  return cudaGetLastError();
+  return launch_pdl(k_page_table, grid, dim3(kTabThreads), 0, s, lens, B, page_size, max_pages, n_pages, pool, n_pool,
+                    first, per, table, held, next, status);
 }
 
 cudaError_t launch_slot_map(const int32_t *table, int B, int max_pages, int page_size, int n_pages,
@@ -288,25 +289,24 @@ cudaError_t launch_slot_map(const int32_t *table, int B, int max_pages, int page
                             int max_rows, int32_t *row_start, int32_t *row_pos, int32_t *slot, int32_t *status,
                             cudaStream_t s) {
   const int grid = max_rows > 0 ? (int)(((long long)max_rows + kMapRows - 1) / kMapRows) : 1;
-  launch_pdl(k_slot_map, dim3(grid), dim3(kMapThreads), 0, s, table, B, max_pages, page_size, n_pages, count, pos,
-             pos_stride, first, max_rows, row_start, row_pos, slot, status);
-  return cudaGetLastError();
+  return launch_pdl(k_slot_map, dim3(grid), dim3(kMapThreads), 0, s, table, B, max_pages, page_size, n_pages, count,
+                    pos, pos_stride, first, max_rows, row_start, row_pos, slot, status);
 }
 
 cudaError_t launch_paged_write(const float *qkv, int max_rows, const int32_t *n_rows, const int32_t *row_pos,
                                const int32_t *slot, const float2 *rope, int max_pos, int n_heads,
                                const dcu_pages &pages, void *q, int32_t *status, cudaStream_t s) {
+  // a row's items in as few slices as fit a CTA, in equal parts
   const int items = (n_heads + 2 * pages.n_kv_heads) * (pages.head_dim / 16);
-  int gy = (items + kWriteThreads * kWriteItems - 1) / (kWriteThreads * kWriteItems);
-  if (gy > 64) gy = 64;
-  const dim3 grid(max_rows, gy);
+  const int slices = (items + kWriteMax - 1) / kWriteMax;
+  if (slices > 65535) return cudaErrorInvalidValue;
+  const int threads = ((items + slices - 1) / slices + 31) / 32 * 32;
+  const dim3 grid(max_rows, slices);
   if (pages.dtype == DCU_BF16)
-    launch_pdl(k_paged_write<bf16>, grid, dim3(kWriteThreads), 0, s, qkv, max_rows, n_rows, row_pos, slot, rope,
-               max_pos, n_heads, pages, (bf16 *)q, status);
-  else
-    launch_pdl(k_paged_write<float>, grid, dim3(kWriteThreads), 0, s, qkv, max_rows, n_rows, row_pos, slot, rope,
-               max_pos, n_heads, pages, (float *)q, status);
-  return cudaGetLastError();
+    return launch_pdl(k_paged_write<bf16>, grid, dim3(threads), 0, s, qkv, max_rows, n_rows, row_pos, slot, rope,
+                      max_pos, n_heads, pages, (bf16 *)q, status);
+  return launch_pdl(k_paged_write<float>, grid, dim3(threads), 0, s, qkv, max_rows, n_rows, row_pos, slot, rope,
+                      max_pos, n_heads, pages, (float *)q, status);
 }
 
 }  // namespace dcu

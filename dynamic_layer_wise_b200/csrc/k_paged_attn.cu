@@ -672,38 +672,40 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
 // out = sum_i w_i O_i, w_i = 2^(m_i - M) / sum_j 2^(m_j - M) l_j, over its
 // shares i.  An item that begins in range r has its first share there (slot 1,
 // or 0 when it is that range's only segment) and the others in slot 0 of the
-// following ranges.  The cut queries of all items form one line, dealt out to
-// the warps of the launch; when there are fewer queries than CTAs (a single
-// token over a long cache: few queries, many shares), a CTA takes a query and
-// its warps split the shares.  Every sum has a fixed order.
+// following ranges.  A piece of work is 8 neighbouring queries x a quarter of
+// the head dim; lane = (query, group of 4 dims), so a warp's loads are whole
+// 128-byte lines of a share.  The pieces of all items form one line, dealt out
+// to the warps of the launch; when there are fewer than CTAs (a single token
+// over a long cache: few queries, many shares), a CTA takes a piece and its
+// warps split the shares.  Every sum has a fixed order.
 constexpr int kMergeThreads = 256;
 
 template <int DP, class T>
 __global__ void __launch_bounds__(kMergeThreads)
     k_paged_merge(const __grid_constant__ PagedAttnArgs a, int R, int ranges, const float *__restrict__ part_o,
                   const float2 *__restrict__ part_ml, const Share *__restrict__ shares) {
-  constexpr int V = DP == 64 ? 2 : 4, ND = DP == 256 ? 2 : 1;  // dims of a lane: ND vectors of V
-  constexpr int W = kMergeThreads / 32;
+  constexpr int W = kMergeThreads / 32, NI = DP / 64;  // groups of 4 dims per lane
+  constexpr int kBatch = 8 / NI;                       // shares whose loads are in flight together
   pdl_enter();
   __shared__ int s_end[kMaxRanges];
   __shared__ Share s_share[kMaxRanges];
   __shared__ int s_red[32];
-  __shared__ float s_part[W][DP];
-  __shared__ float2 s_pml[W];
+  __shared__ float4 s_part[W][NI][32];
+  __shared__ float2 s_pml[W][8];
   static_assert(kMaxRanges <= kMergeThreads, "one thread per range");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int mine = 0;
   if (tid < ranges) {
     const Share sh = shares[tid];
     s_share[tid] = sh;
-    if (sh.last >= 0) mine = sh.nq;
+    if (sh.last >= 0) mine = 4 * ((sh.nq + 7) / 8);
   }
   int total;
   const int pre = block_exclusive_scan(mine, s_red, &total);
   if (tid < ranges) s_end[tid] = pre + mine;
   __syncthreads();
   const int G = a.n_heads / a.pages.n_kv_heads, hd = a.pages.head_dim;
-  const bool whole = total <= (int)gridDim.x;  // a CTA per query
+  const bool whole = total <= (int)gridDim.x;  // a CTA per piece
   const int step = whole ? gridDim.x : gridDim.x * W;
   for (int i = whole ? blockIdx.x : blockIdx.x * W + warp; i < total; i += step) {
     int r = 0, z = ranges - 1;  // the first range whose end is above i
@@ -713,87 +715,96 @@ __global__ void __launch_bounds__(kMergeThreads)
       else r = m + 1;
     }
     const Share sh = s_share[r];
-    const int qr = i - (s_end[r] - sh.nq);
-    const int i0 = whole ? r + warp : r, di = whole ? W : 1;
-    // this warp's shares: r + warp, + W, ... or all of them, kBatch at a time (their O is loaded before the weights
-    // are known)
-    constexpr int kBatch = 8;
-    float M = -INFINITY, L = 0.f, acc[ND][V];
+    const int piece = i - (s_end[r] - 4 * ((sh.nq + 7) / 8));
+    const int qr = (piece >> 2) * 8 + (lane & 7);
+    const int d0 = (piece & 3) * (DP / 4) + (lane >> 3) * 4;  // the lane's dims: d0 + 16 n .. + 3
+    const bool in = qr < sh.nq;
+    float M = -INFINITY, L = 0.f, acc[NI][4];
 #pragma unroll
-    for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] = 0.f;
-    for (int j0 = i0; j0 <= sh.last; j0 += kBatch * di) {
-      const int j = j0 + lane * di;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < kBatch && j <= sh.last) ml = part_ml[((size_t)j * 2 + (j == r ? sh.slot : 0)) * R + qr];
-      float v[kBatch][ND][V];
+    for (int n = 0; n < NI; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    const int di = whole ? W : 1;
+    for (int j0 = whole ? r + warp : r; j0 <= sh.last; j0 += kBatch * di) {
+      float2 ml[kBatch];
+      float4 v[kBatch][NI];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int jj = j0 + k * di;
-        if (jj > sh.last) break;
-        const size_t share = (size_t)jj * 2 + (jj == r ? sh.slot : 0);
+        const int j = j0 + k * di;
+        const size_t share = (size_t)j * 2 + (j == r ? sh.slot : 0);
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (j <= sh.last && in) {
+          ml[k] = part_ml[share * R + qr];
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const float *o = part_o + share_at(share, R, DP, qr, d * 128 + lane * V);
-          if constexpr (V == 4) *reinterpret_cast<float4 *>(v[k][d]) = *reinterpret_cast<const float4 *>(o);
-          else *reinterpret_cast<float2 *>(v[k][d]) = *reinterpret_cast<const float2 *>(o);
+          for (int n = 0; n < NI; ++n)
+            v[k][n] = *reinterpret_cast<const float4 *>(part_o + share_at(share, R, DP, qr, d0 + 16 * n));
         }
       }
-      const float m2 = fmaxf(M, warp_max(ml.x));
-      const float f = M == -INFINITY ? 0.f : exp2f(M - m2);
-      const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m2);
-      L = L * f + warp_sum(ml.x == -INFINITY ? 0.f : w * ml.y);
-      M = m2;
+      float m2 = M;
 #pragma unroll
-      for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] *= f;
+      for (int k = 0; k < kBatch; ++k) m2 = fmaxf(m2, ml[k].x);
+      const float f = M == -INFINITY ? 0.f : exp2f(M - m2);
+      M = m2;
+      L *= f;
+#pragma unroll
+      for (int n = 0; n < NI; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][e] *= f;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        if (j0 + k * di > sh.last) break;
-        const float wk = __shfl_sync(0xffffffffu, w, k);
+        if (j0 + k * di > sh.last || !in) break;
+        const float w = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+        L += ml[k].x == -INFINITY ? 0.f : w * ml[k].y;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-          for (int e = 0; e < V; ++e)
-            if (d * 128 + lane * V + e < hd) acc[d][e] += wk * v[k][d][e];
+        for (int n = 0; n < NI; ++n) {
+          acc[n][0] += w * v[k][n].x;
+          acc[n][1] += w * v[k][n].y;
+          acc[n][2] += w * v[k][n].z;
+          acc[n][3] += w * v[k][n].w;
+        }
       }
     }
-    if (whole) {  // join the warps
+    if (whole) {  // join the warps, in order
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s_part[warp][d * 128 + lane * V + e] = acc[d][e];
-      if (lane == 0) s_pml[warp] = make_float2(M, L);
+      for (int n = 0; n < NI; ++n) s_part[warp][n][lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+      if (lane < 8) s_pml[warp][lane] = make_float2(M, L);
       __syncthreads();
-      M = -INFINITY;
-      for (int k = 0; k < W; ++k) M = fmaxf(M, s_pml[k].x);
-      L = 0.f;
+      if (warp == 0) {
+        M = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < ND * V; ++e) acc[e / V][e % V] = 0.f;
-      for (int k = 0; k < W; ++k) {
-        const float w = s_pml[k].x == -INFINITY ? 0.f : exp2f(s_pml[k].x - M);
-        L += w * s_pml[k].y;
+        for (int k = 0; k < W; ++k) M = fmaxf(M, s_pml[k][lane & 7].x);
+        L = 0.f;
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
+        for (int n = 0; n < NI; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[d][e] += w * s_part[k][d * 128 + lane * V + e];
+        for (int k = 0; k < W; ++k) {
+          const float2 ml = s_pml[k][lane & 7];
+          const float w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+          L += ml.x == -INFINITY ? 0.f : w * ml.y;
+#pragma unroll
+          for (int n = 0; n < NI; ++n) {
+            const float4 x = s_part[k][n][lane];
+            acc[n][0] += w * x.x;
+            acc[n][1] += w * x.y;
+            acc[n][2] += w * x.z;
+            acc[n][3] += w * x.w;
+          }
+        }
       }
       __syncthreads();
       if (warp != 0) continue;
     }
+    if (!in) continue;
     const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
     const int pq = sh.q0 + qr, row = sh.row0 + pq / G, h = sh.kvh * G + pq % G;
-    T *dst = static_cast<T *>(a.out) + ((size_t)row * a.n_heads + h) * hd;
+    T *dst = static_cast<T *>(a.out) + ((size_t)row * a.n_heads + h) * hd + d0;
 #pragma unroll
-    for (int d = 0; d < ND; ++d) {
-      const int at = d * 128 + lane * V;
-      if (at >= hd) continue;
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int e = 0; e < V; e += 2)
-          *reinterpret_cast<uint32_t *>(dst + at + e) = pack2(acc[d][e] * inv, acc[d][e + 1] * inv);
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) dst[at + e] = from_f<T>(acc[d][e] * inv);
-      }
+    for (int n = 0; n < NI; ++n) {
+      if (d0 + 16 * n >= hd) continue;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2 *>(dst + 16 * n) =
+            make_uint2(pack2(acc[n][0] * inv, acc[n][1] * inv), pack2(acc[n][2] * inv, acc[n][3] * inv));
+      else
+        *reinterpret_cast<float4 *>(dst + 16 * n) =
+            make_float4(acc[n][0] * inv, acc[n][1] * inv, acc[n][2] * inv, acc[n][3] * inv);
     }
   }
 }
