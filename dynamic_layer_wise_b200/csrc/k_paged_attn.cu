@@ -36,12 +36,12 @@ namespace {
 template <int DP, bool F32, int NT>
 struct Cfg {
   static constexpr int kKB = F32 ? 8 : 16;                       // keys of a block
-  static constexpr int kW = DP == 256 ? 4 : 8;                   // warps
+  static constexpr int kW = DP == 256 ? 4 : F32 ? 12 : 8;  // warps
   static constexpr int kR = 8 * NT;                              // queries of a tile: NT groups of 8
   static constexpr int kEs = F32 ? 4 : 2;                        // element size
   static constexpr int kRow = DP * kEs;                          // bytes of a key row
   static constexpr int kStage = 2 * kKB * kRow;                  // K and V of a block
-  static constexpr int kNst = DP == 64 ? 5 : 3;                  // ring stages of a warp
+  static constexpr int kNst = DP == 256 ? 3 : F32 ? (DP == 64 ? 4 : 2) : (DP == 64 ? 5 : 3);  // ring stages of a warp
   static constexpr int kQPitch = kRow + 16;                      // padded query row
   static constexpr int kRing = kW * kNst * kStage;
   static constexpr int kQ = kR * kQPitch;
@@ -49,6 +49,7 @@ struct Cfg {
   static constexpr int kP = F32 ? kW * 64 * 4 : 0;               // float32: P of a block, per warp
   static constexpr int kSmem = kRing + kQ + kRed + kP + 1024;  // + alignment of the ring
   static constexpr int kThreads = 32 * kW;
+  static_assert(kSmem + 2800 <= 227 * 1024, "dynamic and static shared memory of an SM");
   static constexpr int kND = F32 ? (DP > 128 ? DP / 128 : 1) : 0;  // float32: 4-dim chunks of O per lane and query
   static constexpr int kAcc = F32 ? 8 * kND : DP / 16;           // float4s of O per lane and query group
 };
@@ -423,33 +424,44 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
           }
         }
       } else {
-        // lane = (key g, quarter t): its quarter of the 16-byte chunks of the row, all 8 queries; odd keys take the
-        // two halves of a 128-byte row in the other order, so a quarter warp's 8 chunks fall in 8 bank groups
+        // lane = (keys 2 (lane / 8) and + 1, every 8th 16-byte chunk of the row), all 8 queries: a query chunk read from
+        // shared memory serves two keys (reading the queries again for every key would bound the loop), and the 8 lanes
+        // of a key read 8 bank groups
         const uint8_t *kr = sm + (kt - sm32);
-        float s[8];
+        const int t8 = lane & 7, ka = (lane >> 3) * 2;
+        float s[2][8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s[r] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < CPR / 4; ++i) {
-          const int c = 4 * (i ^ (g & 1)) + t;
-          const float4 kv = *reinterpret_cast<const float4 *>(kr + kv_off<KB>(g, c));
+        for (int r = 0; r < 8; ++r) s[0][r] = s[1][r] = 0.f;
+#pragma unroll 2
+        for (int i = 0; i < CPR / 8; ++i) {
+          const int c = 8 * i + t8;
+          const float4 k0 = *reinterpret_cast<const float4 *>(kr + kv_off<KB>(ka, c));
+          const float4 k1 = *reinterpret_cast<const float4 *>(kr + kv_off<KB>(ka + 1, c));
 #pragma unroll
           for (int r = 0; r < 8; ++r) {
             const float4 qv = *reinterpret_cast<const float4 *>(q_sm + r * C::kQPitch + c * 16);
-            s[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[r]))));
+            s[0][r] = fmaf(qv.x, k0.x, fmaf(qv.y, k0.y, fmaf(qv.z, k0.z, fmaf(qv.w, k0.w, s[0][r]))));
+            s[1][r] = fmaf(qv.x, k1.x, fmaf(qv.y, k1.y, fmaf(qv.z, k1.z, fmaf(qv.w, k1.w, s[1][r]))));
           }
         }
+        // sums over the 8 lanes, each step keeping half of the values: bit 2 of the lane takes its key, bits 1 and 0 the
+        // queries, which ends with key g = lane / 4 and queries 2 t, 2 t + 1
         float x[2];
-        const bool v = (mask >> g) & 1u;
+        {
+          float h4[8], h2[4];
+          const bool b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
-          s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-        }
+          for (int r = 0; r < 8; ++r)
+            h4[r] = (b2 ? s[1][r] : s[0][r]) + __shfl_xor_sync(0xffffffffu, b2 ? s[0][r] : s[1][r], 4);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {  // the lane's queries 2 t, 2 t + 1
-          const float sv = t == 0 ? s[c] : t == 1 ? s[2 + c] : t == 2 ? s[4 + c] : s[6 + c];
-          x[c] = v ? sv * a.scale_log2 : -INFINITY;
+          for (int r = 0; r < 4; ++r)
+            h2[r] = (b1 ? h4[4 + r] : h4[r]) + __shfl_xor_sync(0xffffffffu, b1 ? h4[r] : h4[4 + r], 2);
+          const bool v = (mask >> g) & 1u;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float sv = (b0 ? h2[2 + c] : h2[c]) + __shfl_xor_sync(0xffffffffu, b0 ? h2[c] : h2[2 + c], 1);
+            x[c] = v ? sv * a.scale_log2 : -INFINITY;
+          }
         }
         float mx[2] = {x[0], x[1]};
 #pragma unroll
@@ -878,8 +890,12 @@ cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const S
 }
 
 // Queries per sequence and kv head, on average, above which the tcgen05 kernel
-// is taken.
-constexpr long long kTcMinQueries = 32;
+// is taken.  Measured, this kernel / that one: 1 x 1024 keys, 32 heads x 128:
+// 16 queries 16.3 / 16.1 us, 32 queries 20.4 / 17.2; 1 x 8192 keys: 16 queries
+// 54.2 / 54.6, 32 queries 68.3 / 56.3; 64 x 2000 keys of 28/4 heads: 14 queries
+// 94 / 113, 28 queries 115 / 113; 128 x 100 keys, 8 heads x 64: 16 queries
+// 44 / 52, 32 queries 60 / 55.
+constexpr long long kTcMinQueries = 24;
 
 int64_t paged_attention_workspace(const dcu_pages &p) {
   const int dp = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
