@@ -1,32 +1,34 @@
 // Paged attention of many query rows per sequence on the 5th-gen tensor cores
 // (bf16, head_dim up to 128).  Same line of work, shares and merge as
-// k_paged_attn.cu, with items of up to 256 queries (two MMA tiles of 128, one
-// TMEM lane per query) and units of 128 keys:
+// k_paged_attn.cu, with items of up to 128 queries (one TMEM lane each) and
+// units of 128 keys, worked in sub-chunks of 64:
 //
-//   warp 0     TMA producer: the pages of a chunk of 128 keys, boxes of
-//              box_keys slots x 64 dims (128-byte swizzle), K and V rings of
-//              two stages; a box past the sequence's end or on a bad page is
-//              read at a page coordinate outside the tensor, i.e. as zeros
-//   warps 1, 2 MMA issuers of tile A and of tile B (one thread each): S_t =
-//              Q_t K^T (M = 128 queries, N = 128 keys) and O_t += P_t V (P_t in
-//              tensor memory, V MN-major)
-//   warps 4-11 and 12-19  softmax of tile A and of tile B: thread = (query, half
-//              of the sub-chunk's keys)
+//   warp 0      TMA producer: the pages of a chunk of 128 keys, boxes of `box`
+//               slots x 64 dims (128-byte swizzle), into a K and a V ring; a box
+//               past the sequence's end or on a bad page is read at a page
+//               coordinate outside the tensor, i.e. as zeros
+//   warp 1      MMA issuer (one elected thread): S_u = Q K_u^T (M = 128 queries,
+//               N = 64 keys) into one of four score buffers in tensor memory,
+//               three sub-chunks ahead, and O += P_u V_u (P_u in tensor memory,
+//               V MN-major)
+//   warps 4-19  softmax, four sets of four warps: set u % 4 takes sub-chunk u, a
+//               thread is a query and has all 64 keys
 //
-// A chunk is worked in two sub-chunks of 64 keys, each with a TMEM score buffer
-// of its own per tile, so S of the next sub-chunk is there when the softmax
-// gets to it and only the softmax is on the critical path; the two tiles share
-// every K and V stage.  An item of at most 128 queries gives both tiles the
-// same queries and every other chunk, each with its own maximum, sum and O, and
-// the two are joined at its end.
-// TMEM: two score buffers of 64 columns for A, two for B, O_A and O_B of 128
-// columns; P (bf16 pairs) overwrites scores that the same thread has read.
+// The only thing that goes from one sub-chunk to the next is the running maximum
+// (O, P and the sums share it): a set waits for its predecessor's maximum, not
+// for its exponentials, so four sub-chunks are in work at a time and neither the
+// MMA's nor the softmax's latency is on the critical path.  (Two tiles of 128
+// queries taking turns on two buffers each, measured before: 1.3 us per 128
+// queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
+// TMEM: four score buffers of 64 columns, O of head_dim columns; P (bf16 pairs)
+// overwrites the second half of its scores, which are in registers by then.
 // P is rounded to bf16 once, as in the dense attention of a step: a second
-// product for the low part would cost half as much again on the pipe that
-// bounds this kernel.
+// product for the low part would cost half as much again on the tensor pipe.
 //
 // Every mbarrier wait is bounded; on expiry the CTA sets DCU_ST_TIMEOUT, drains
-// its copies and MMAs in flight, frees TMEM and exits.
+// its copies and MMAs in flight, frees TMEM and exits.  A parity wait is only
+// sound for a phase that is the current or the last one of its barrier; where
+// that is not plain from the order of the waits, a comment says why it holds.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -35,18 +37,18 @@ namespace {
 
 constexpr int kKC = 128;              // keys of a unit
 constexpr int kSub = 64;              // keys of a sub-chunk
-constexpr int kStages = 2;            // K and V ring depth
-constexpr int kSoftWarps = 8;         // per tile
+constexpr int kKStages = 3, kVStages = 2;  // ring depths (chunks)
+constexpr int kSets = 4;              // softmax sets = score buffers
 constexpr int kSoft0 = 4;             // first softmax warp
-constexpr int kWarps = kSoft0 + 2 * kSoftWarps;
+constexpr int kWarps = kSoft0 + 4 * kSets;
 constexpr int kThreads = 32 * kWarps;
 
 template <int DP>
 struct TcCfg {
-  static constexpr uint32_t kTile = 128u * DP * 2u;  // a Q tile, or K or V of a chunk: DP / 64 blocks of 16 KB
-  static constexpr uint32_t kSmem = (2 + 2 * kStages) * kTile + 1024u;
+  static constexpr uint32_t kTile = 128u * DP * 2u;  // the Q tile, or K or V of a chunk: DP / 64 blocks of 16 KB
+  static constexpr uint32_t kSmem = (1 + kKStages + kVStages) * kTile + 1024u;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kO = 256;                // O_t at column 256 + 128 t
+  static constexpr uint32_t kO = 256;                // O at column 256
 };
 
 __device__ __forceinline__ uint32_t tile_off(int r, int c) {  // 16-byte chunk c of row r
@@ -70,6 +72,12 @@ __device__ __forceinline__ uint32_t packb(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], uint32_t valid) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (!((valid >> c) & 1u)) r[c] = 0xff800000u;  // -inf
+}
+
 // true in one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -83,56 +91,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap vmap, int head_first, int box, float *__restrict__ part_o,
                     float2 *__restrict__ part_ml, Share *__restrict__ shares) {
   using C = TcCfg<DP>;
-  constexpr int R = kTcQueries, OC = DP / 2;  // O columns of a half
+  constexpr int R = kTcQueries;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[4 * kStages + 16];
+  __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kSets + 3 + 4 * kSets];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
   __shared__ Place s_place;
-  __shared__ float s_mx[2][2][2][128];  // [sub-chunk parity][tile][half] maximum of the half's keys
-  __shared__ float s_l[2][2][128];      // [tile][half] share of the row sum
-  __shared__ float s_m[2][128];         // [tile] final row maximum
-  __shared__ uint32_t s_bad[4];         // [chunk % 4] boxes of the chunk on bad pages
+  __shared__ float s_max[kSets][128];   // [set] running maximum after the set's sub-chunk
+  __shared__ float2 s_ml[kSets][128];   // [set] (maximum, sum) at the end of a segment
+  __shared__ uint32_t s_bad[8];         // [chunk % 8] boxes of the chunk on bad pages
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
-  const uint32_t q_s = sbase, k_s = sbase + 2 * C::kTile, v_s = k_s + kStages * C::kTile;
+  const uint32_t q_s = sbase, k_s = sbase + C::kTile, v_s = k_s + kKStages * C::kTile;
   const uint32_t bar0 = smem_u32(bars);
   auto K_FULL = [&](uint32_t s) { return bar0 + 8u * s; };
-  auto K_EMPTY = [&](uint32_t s) { return bar0 + 8u * (kStages + s); };
-  auto V_FULL = [&](uint32_t s) { return bar0 + 8u * (2 * kStages + s); };
-  auto V_EMPTY = [&](uint32_t s) { return bar0 + 8u * (3 * kStages + s); };
-  auto S_FULL = [&](int t, uint32_t b) { return bar0 + 8u * (4 * kStages + 2 * t + b); };
-  auto P_FULL = [&](int t, uint32_t b) { return bar0 + 8u * (4 * kStages + 4 + 2 * t + b); };
-  auto PV_DONE = [&](int t) { return bar0 + 8u * (4 * kStages + 8 + t); };
-  auto DRAIN = [&](int t) { return bar0 + 8u * (4 * kStages + 10 + t); };
-  const uint32_t Q_FULL = bar0 + 8u * (4 * kStages + 12), O_FINAL = Q_FULL + 8u;
-  // tile A's softmax warps, per segment of two tiles whose last chunk ends inside a page: V's rows there are cleared.
-  // (Tile B may be a chunk ahead or behind, so P_FULL of tile A would not do: a parity wait is only sound within one
-  // phase.)
-  const uint32_t V_CLEAR = Q_FULL + 16u, A_BEGUN = Q_FULL + 24u;  // A_BEGUN: tile A has its first scores of a segment
+  auto K_EMPTY = [&](uint32_t s) { return bar0 + 8u * (kKStages + s); };
+  auto V_FULL = [&](uint32_t s) { return bar0 + 8u * (2 * kKStages + s); };
+  auto V_EMPTY = [&](uint32_t s) { return bar0 + 8u * (2 * kKStages + kVStages + s); };
+  const uint32_t bar1 = bar0 + 8u * (2 * (kKStages + kVStages));
+  auto S_FULL = [&](uint32_t b) { return bar1 + 8u * b; };                   // scores of buffer b are there
+  auto P_FULL = [&](uint32_t b) { return bar1 + 8u * (kSets + b); };         // its P is there
+  auto PV_DONE = [&](uint32_t b) { return bar1 + 8u * (2 * kSets + b); };    // its P V is in O
+  const uint32_t Q_FULL = bar1 + 8u * (3 * kSets), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;
+  auto MAX = [&](uint32_t set, int q4) { return Q_FULL + 24u + 8u * (set * 4u + (uint32_t)q4); };  // s_max[set] of 32 rows
 
   if (tid == 0) {
-    // a stage is empty, and a segment final, once both tiles say so (a tile that has the chunk to itself, twice)
-    for (uint32_t s = 0; s < kStages; ++s) {
-      mbar_init(K_FULL(s), 1);
-      mbar_init(K_EMPTY(s), 2);
-      mbar_init(V_FULL(s), 1);
-      mbar_init(V_EMPTY(s), 2);
+    for (uint32_t i = 0; i < 2 * (kKStages + kVStages); ++i) mbar_init(bar0 + 8u * i, 1);
+    for (uint32_t b = 0; b < kSets; ++b) {
+      mbar_init(S_FULL(b), 2);  // the scores (commit), and the issuer itself (it has seen the chunk's K_FULL)
+      mbar_init(P_FULL(b), 4);
+      mbar_init(PV_DONE(b), 1);
+      for (int q = 0; q < 4; ++q) mbar_init(MAX(b, q), 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(DRAIN(t), 1);
-      for (uint32_t b = 0; b < 2; ++b) {
-        mbar_init(S_FULL(t, b), 2);  // the scores (commit), and the issuer itself (it has seen the chunk's K_FULL)
-        mbar_init(P_FULL(t, b), kSoftWarps);
-      }
-      mbar_init(PV_DONE(t), 1);
-    }
-    mbar_init(Q_FULL, 2 * kSoftWarps);
-    mbar_init(O_FINAL, 2);
-    mbar_init(V_CLEAR, kSoftWarps);
-    mbar_init(A_BEGUN, kSoftWarps);
+    mbar_init(Q_FULL, 4 * kSets);
+    mbar_init(O_FINAL, 1);
+    mbar_init(DRAIN, 1);
     abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -165,10 +160,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return mine && key < ld.s.nk ? a.table[(size_t)ld.b * a.max_pages + div_page(a, (unsigned)key)] : -1;
     };
     int pg = look();
-    uint32_t issued = 0;
+    uint32_t g = 0, nk_ = 0, nv_ = 0;  // chunk of the CTA; K and V copies issued
     bool ok = true;
-    for (long long u = rg.u0; u < rg.u1 && ok; ++u) {
-      const uint32_t st = issued % kStages, ph = ((issued / kStages) & 1u) ^ 1u;
+    for (long long u = rg.u0; u < rg.u1 && ok; ++u, ++g) {
       const int key = ld.blk * kKC + my * box, kvh = ld.kvh;
       const bool in = mine && key < ld.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
       if (in && !good && half == 0 && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
@@ -181,113 +175,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         advance<R, kKC>(a, ld, 1);
         pg = look();
       }
-      for (int v = 0; v < 2 && ok; ++v) {
-        ok = __all_sync(0xffffffffu, wait_bounded(v ? V_EMPTY(st) : K_EMPTY(st), ph, abort_v, a.status));
+      {
+        const uint32_t st = g % kKStages;
+        ok = __all_sync(0xffffffffu, wait_bounded(K_EMPTY(st), ((g / kKStages) & 1u) ^ 1u, abort_v, a.status));
         if (!ok) break;
-        const uint32_t bar = v ? V_FULL(st) : K_FULL(st);
         if (lane == 0) {
-          // read by the softmax once it has S of the chunk; by then tile A and B are past the entry's last use
-          if (!v) s_bad[issued & 3u] = bad;
-          mbar_expect_tx(bar, C::kTile);
+          s_bad[g & 7u] = bad;  // read by the softmax with the scores of the chunk; eight chunks later all have
+          mbar_expect_tx(K_FULL(st), C::kTile);
         }
         __syncwarp();
-        if (mine) tma_box((v ? v_s : k_s) + st * C::kTile + dst, v ? &vmap : &kmap, half * 64, c1, c2, w, bar);
-        if (v) ++issued;
+        if (mine) tma_box(k_s + st * C::kTile + dst, &kmap, half * 64, c1, c2, w, K_FULL(st));
+        ++nk_;
+      }
+      {
+        const uint32_t st = g % kVStages;
+        ok = __all_sync(0xffffffffu, wait_bounded(V_EMPTY(st), ((g / kVStages) & 1u) ^ 1u, abort_v, a.status));
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(V_FULL(st), C::kTile);
+        __syncwarp();
+        if (mine) tma_box(v_s + st * C::kTile + dst, &vmap, half * 64, c1, c2, w, V_FULL(st));
+        ++nv_;
       }
     }
-    if (!ok) {  // wait, bounded, for the copies still in flight
-      for (uint32_t s = 0; s < kStages; ++s) {
-        const uint32_t nk = issued > s ? (issued - 1 - s) / kStages : 0;  // last full phase of the stage
-        if (issued > s) {
-          wait_drain(K_FULL(s), nk & 1u);
-          wait_drain(V_FULL(s), nk & 1u);
-        }
-      }
-      const uint32_t s = issued % kStages;  // a K load whose V was not issued (ends at once if there was none)
-      wait_drain(K_FULL(s), (issued / kStages) & 1u);
+    if (!ok) {  // wait, bounded, for the copies still in flight: the last phase of every stage
+      for (uint32_t s = 0; s < kKStages; ++s)
+        if (nk_ > s) wait_drain(K_FULL(s), ((nk_ - 1 - s) / kKStages) & 1u);
+      for (uint32_t s = 0; s < kVStages; ++s)
+        if (nv_ > s) wait_drain(V_FULL(s), ((nv_ - 1 - s) / kVStages) & 1u);
     }
-  } else if (warp == 1 || warp == 2) {
-    // ---- MMA issuer of tile t: the warp runs as one, an elected lane issues
-    const int t = warp - 1;
+  } else if (warp == 1) {
+    // ---- MMA issuer: the warp runs as one, an elected lane issues
     const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
-    const uint32_t s_tm = tmem + 128u * t, o_tm = tmem + C::kO + 128u * t;
     const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
-    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages (and of the Q tiles)
+    constexpr uint64_t kStep = C::kTile >> 4, kHalf = (uint64_t)(kSub * 128 >> 4);  // descriptor distances
     bool ok = true, any = false;
-    uint32_t g = 0, nseg = 0;      // chunks of the CTA, segments
-    uint32_t u = 0, clears = 0;    // sub-chunks of this tile, V_CLEAR phases
+    uint32_t g = 0, nseg = 0;  // chunks of the CTA before the segment, segments
     auto wait = [&](uint32_t bar, uint32_t par) {
       ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
       return ok;
     };
-    // scores of sub-chunk h of the chunk in stage st, into buffer h
-    auto issue_s = [&](uint32_t st, uint32_t h, bool alone) {
-      const uint64_t kd = kd0 + st * kStep + h * (uint64_t)(kSub * 128 >> 4), qq = alone ? qd : qd + t * kStep;
+    // scores of sub-chunk i of the segment
+    auto issue_s = [&](int i) {
+      const uint32_t gj = g + (uint32_t)(i >> 1), st = gj % kKStages, h = (uint32_t)(i & 1), b = (2 * g + i) & 3u;
+      if (h == 0 && !wait(K_FULL(st), gj / kKStages)) return;
+      tc_fence_after();
+      const uint64_t kd = kd0 + st * kStep + h * kHalf;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk) {
           const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
-          tc_mma(s_tm + h * 64u, qq + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+          tc_mma(tmem + b * 64u, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
         }
-        tc_commit(S_FULL(t, h));
-        mbar_arrive(S_FULL(t, h));
-        if (h) {
-          tc_commit(K_EMPTY(st));
-          if (alone) tc_commit(K_EMPTY(st));
-        }
+        tc_commit(S_FULL(b));
+        mbar_arrive(S_FULL(b));
+        if (h) tc_commit(K_EMPTY(st));
       }
       __syncwarp();
       any = true;
     };
     for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
       const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-      const int n = (int)(s1 - s0);
-      const bool alone = min(seg.s.tq, seg.s.nq - seg.tile * seg.s.tq) <= 128;
-      const int j0 = alone ? t : 0, dj = alone ? 2 : 1;  // this tile's chunks: j0, j0 + dj, ...
-      // every segment in turn, also one without a chunk of this tile: a wait may be at most one phase behind
+      const int n = (int)(s1 - s0), ns = 2 * n;
       if (!wait(Q_FULL, nseg)) break;
-      if (j0 < n) {
-        const uint32_t st = (g + j0) % kStages;
-        if (!wait(K_FULL(st), (g + j0) / kStages)) break;
-        // tile B starts half a sub-chunk late, so that the two tiles' exponentials take turns
-        if (!alone && t == 1 && n > 2 && !wait(A_BEGUN, nseg)) break;
+      // Three sub-chunks ahead.  A buffer's last P V (of the segment before, or of sub-chunk i - 4) has been waited for.
+      for (int i = 0; i < min(3, ns) && ok; ++i) issue_s(i);
+      for (int i = 0; i < ns && ok; ++i) {
+        const uint32_t u = 2 * g + (uint32_t)i, b = u & 3u, gj = g + (uint32_t)(i >> 1), st = gj % kVStages;
+        if (!wait(P_FULL(b), u >> 2) || ((i & 1) == 0 && !wait(V_FULL(st), gj / kVStages))) break;
         tc_fence_after();
-        issue_s(st, 0, alone);
-        issue_s(st, 1, alone);
-      }
-      for (int j = j0; j < n && ok; j += dj) {
-        const uint32_t gj = g + (uint32_t)j, st = gj % kStages, gn = gj + (uint32_t)dj, sn = gn % kStages;
-        const bool last = j + dj >= n;
-        for (uint32_t h = 0; h < 2; ++h, ++u) {
-          if (!wait(P_FULL(t, h), u >> 1)) break;
-          if (h == 0) {
-            if (!wait(V_FULL(st), gj / kStages)) break;
-            // the rows of V past the end of an item's last chunk are cleared by the softmax warps of tile A, or of the
-            // one tile that takes the chunk, before their P_FULL (tile B: V_CLEAR)
-            if (!alone && t == 1 && seg.s.nk - (seg.blk + j) * kKC < kKC && !wait(V_CLEAR, clears++)) break;
-          }
-          tc_fence_after();
-          const uint64_t vd = vd0 + st * kStep + h * (uint64_t)(kSub * 128 >> 4);
-          if (elect_one()) {
+        const uint64_t vd = vd0 + st * kStep + (uint64_t)(i & 1) * kHalf;
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kSub / 16; ++kk)
-              tc_mma_ts(o_tm, s_tm + h * 64u + (uint32_t)((kk >> 1) * 32 + 16 + (kk & 1) * 8),
-                        vd + (uint64_t)(kk * (2048 >> 4)), id_o, (j > j0 || h > 0 || kk > 0) ? 1u : 0u);
-            tc_commit(PV_DONE(t));
-            if (h) {
-              tc_commit(V_EMPTY(st));
-              if (alone) tc_commit(V_EMPTY(st));
-            }
-          }
-          __syncwarp();
-          // the buffer's next scores overwrite P: after P V has read it
-          if ((!last && h == 0 && !wait(K_FULL(sn), gn / kStages)) || !wait(PV_DONE(t), u)) break;
-          if (!last) {
-            tc_fence_after();
-            issue_s(sn, h, alone);
-          }
+          for (int kk = 0; kk < kSub / 16; ++kk)
+            tc_mma_ts(tmem + C::kO, tmem + b * 64u + 32u + (uint32_t)(kk * 8), vd + (uint64_t)(kk * (2048 >> 4)), id_o,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(PV_DONE(b));
+          if (i & 1) tc_commit(V_EMPTY(st));
+        }
+        __syncwarp();
+        if (i + 3 < ns) {
+          // the buffer of sub-chunk i + 3 is that of i - 1, whose P V must have read its P
+          if (i > 0 && !wait(PV_DONE((u - 1) & 3u), (u - 1) >> 2)) break;
+          issue_s(i + 3);
         }
       }
+      if (!ok) break;
+      // the last four P V of the segment: waited for in order, so that no PV_DONE wait falls a phase behind
+      for (int i = max(0, ns - 4); i < ns && ok; ++i) wait(PV_DONE((2 * g + i) & 3u), (2 * g + (uint32_t)i) >> 2);
       if (!ok) break;
       if (elect_one()) tc_commit(O_FINAL);
       __syncwarp();
@@ -296,180 +270,173 @@ __global__ void __launch_bounds__(kThreads, 1)
       s0 = s1;
     }
     if (!ok && any) {
-      if (elect_one()) tc_commit(DRAIN(t));
+      if (elect_one()) tc_commit(DRAIN);
       __syncwarp();
-      wait_drain(DRAIN(t), 0);
+      wait_drain(DRAIN, 0);
     }
   } else if (warp >= kSoft0) {
     // ---- softmax
-    const int t = (warp - kSoft0) / kSoftWarps, pt = ((warp - kSoft0) % kSoftWarps) / 4, q4 = warp & 3;
-    const int qi = q4 * 32 + lane;                       // query of the tile = TMEM lane
+    const uint32_t set = (uint32_t)(warp - kSoft0) / 4u;
+    const int q4 = warp & 3, qi = q4 * 32 + lane;        // query of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t s_tm = tmem + 128u * t + lane_off, o_tm = tmem + C::kO + 128u * t + lane_off + (uint32_t)(pt * OC);
+    const uint32_t s_tm = tmem + set * 64u + lane_off, o_tm = tmem + C::kO + lane_off;
     const int st_id = tid - 32 * kSoft0;
     const float sc = a.scale_log2;
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + t * 4 + q4) : "memory"); };
-    uint32_t u = 0, g = 0, nseg = 0;  // sub-chunks of this tile, chunks of the CTA, segments
+    uint32_t g = 0, nseg = 0;  // chunks of the CTA before the segment, segments
     bool alive = true;
-    constexpr int kPart = kSub / 2;   // keys of a thread in a sub-chunk
     for (long long s0 = rg.u0; s0 < rg.u1; ++nseg) {
       const Seq &sq = seg.s;
       const long long s1 = min(rg.u1, s0 + (sq.nblk - seg.blk));
-      const int n = (int)(s1 - s0);
+      const int n = (int)(s1 - s0), ns = 2 * n;
       const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
-      const bool alone = nq <= 128;
       const Pairs pairs(sq, q0, G);
-      const int j0 = alone ? t : 0, dj = alone ? 2 : 1;  // this tile's chunks: j0, j0 + dj, ...
-      // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read
-      // theirs (O_FINAL)
-      {
-        const int rows = nq > 128 ? 256 : 128;
-        for (int i = st_id; i < rows * (DP / 8); i += 64 * kSoftWarps) {
-          const int r = i / (DP / 8), c = i - r * (DP / 8);
-          const bool in = r < nq && c * 8 < hd;
-          load_query16(q_s + (uint32_t)(r >> 7) * C::kTile + tile_off(r & 127, c),
-                       static_cast<const bf16 *>(a.q) + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0),
-                       in);
-        }
-        load_query_wait();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(Q_FULL);
+      // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read theirs
+      // (O_FINAL)
+      for (int i = st_id; i < 128 * (DP / 8); i += 128 * kSets) {
+        const int r = i / (DP / 8), c = i - r * (DP / 8);
+        const bool in = r < nq && c * 8 < hd;
+        load_query16(q_s + tile_off(r, c),
+                     static_cast<const bf16 *>(a.q) + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0),
+                     in);
       }
-      float m_run = -INFINITY, l_run = 0.f;
-      const int ns = j0 < n ? 2 * ((n - j0 + dj - 1) / dj) : 0;  // this tile's sub-chunks
-      const bool used = (alone ? 0 : t * 128) + q4 * 32 < nq;     // this warp has queries
-      for (int i = 0; i < ns; ++i, ++u) {
-        const int j = j0 + (i >> 1) * dj, key0 = (seg.blk + j) * kKC + (i & 1) * kSub;
-        const uint32_t hb = (uint32_t)(i & 1), s_buf = s_tm + hb * 64u;
-        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(t, hb), (u >> 1) & 1u, abort_v, a.status));
-        const int nv = sq.nk - key0 - pt * kPart;  // valid keys of this thread
-        const uint32_t gj = g + (uint32_t)j;
-        if (t == 0 && i == 0 && lane == 0) mbar_arrive(A_BEGUN);
+      load_query_wait();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(Q_FULL);
+      const bool used = q4 * 32 < nq;             // this warp has queries
+      float m_own = -INFINITY, l_run = 0.f;       // the maximum of this set's last sub-chunk, its share of the sum
+      for (int i = (int)((set - 2 * g) & 3u); i < ns; i += kSets) {
+        const uint32_t u = 2 * g + (uint32_t)i, gj = g + (uint32_t)(i >> 1);
+        const int c0 = (i & 1) * kSub;                           // the sub-chunk's first key in the chunk
+        const int left = sq.nk - (seg.blk + (i >> 1)) * kKC;     // keys of the sequence from the chunk's first on
+        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(set), (u >> 2) & 1u, abort_v, a.status));
+        if (!alive) continue;  // nothing is handed on any more: every wait now fails
         if (used) {
-        uint32_t sr[kPart];  // raw scores: the scale (> 0) commutes with the maximum and enters the exponent
-        float mc = -INFINITY;
-        if (alive) {
           tc_fence_after();
-          tmem_ld32_issue(s_buf + (uint32_t)(pt * kPart), sr);
-          tmem_wait_ld_tie32(sr);
-          const uint32_t bad = s_bad[gj & 3u];
-          if (nv < kPart || bad) {
-            uint32_t valid = nv >= kPart ? ~0u : nv <= 0 ? 0u : (1u << nv) - 1u;
-            const int k0 = (i & 1) * kSub + pt * kPart;  // this thread's keys in the chunk: one box, or two of 16
-            if ((bad >> (k0 / box)) & 1u) valid &= box >= kPart ? 0u : ~0u << box;
-            if (box < kPart && ((bad >> (k0 / box + 1)) & 1u)) valid &= (1u << box) - 1u;
-#pragma unroll
-            for (int c = 0; c < kPart; ++c)
-              if (!((valid >> c) & 1u)) sr[c] = 0xff800000u;  // -inf
+          // Raw scores: the scale (> 0) commutes with the maximum and enters the exponent.  The first 32 keys are read
+          // again for the exponentials rather than kept, which holds the thread within its registers.
+          uint32_t lo = ~0u, hi = ~0u;  // valid keys
+          const uint32_t bad = s_bad[gj & 7u];
+          const bool cut = left < c0 + kSub || bad;
+          if (cut) {
+            unsigned long long v = left >= c0 + kSub ? ~0ull : left <= c0 ? 0ull : (1ull << (left - c0)) - 1ull;
+            for (int x = 0; x < kSub; x += box)
+              if ((bad >> ((c0 + x) / box)) & 1u) v &= ~((box >= kSub ? ~0ull : (1ull << box) - 1ull) << x);
+            lo = (uint32_t)v;
+            hi = (uint32_t)(v >> 32);
           }
+          uint32_t sr[32];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kPart; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
-          mc = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        }
-        s_mx[u & 1][t][pt][qi] = mc;
-        pair_sync();
-        mc = fmaxf(mc, s_mx[u & 1][t][1 - pt][qi]);
-        if (!alive) continue;
-        // The maximum moves only when a sub-chunk exceeds it by more than 8 (log2 units): P stays below 2^8, most
-        // sub-chunks rescale nothing, and P, the sum and O share it.
-        const bool grow = mc > m_run + 8.f;
-        const float m_new = grow ? mc : m_run;
-        const float alpha = grow ? (m_run == -INFINITY ? 0.f : ex2a(m_run - m_new)) : 1.f;
-        if (i > 0 && __any_sync(0xffffffffu, grow)) {
-          // P V of the sub-chunk before must be in O.  The wait is within a phase: P V of the one before that was
-          // complete before S_FULL, and this one's cannot be before its P_FULL.
-          alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE(t), (u - 1) & 1u, abort_v, a.status));
-          if (!alive) continue;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < OC / 16; ++c) {
-            float ov[16];
-            tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
+          for (int hf = 0; hf < 2; ++hf) {
+            tmem_ld32_issue(s_tm + (uint32_t)(hf * 32), sr);
+            tmem_wait_ld_tie32(sr);
+            if (cut) mask32(sr, hf ? hi : lo);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] *= alpha;
-            tmem_st16(o_tm + (uint32_t)(c * 16), ov);
+            for (int c = 0; c < 32; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sr[c]));
           }
-        }
-        m_run = m_new;
-        const float m_use = m_new == -INFINITY ? 0.f : m_new;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          const float mc = sc * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // The predecessor's maximum (its last phase is long over: this set has waited for it, or a segment has ended).
+          float m_old = -INFINITY;
+          if (i > 0) {
+            const uint32_t ps = (set + 3u) & 3u;
+            alive = __all_sync(0xffffffffu, wait_bounded(MAX(ps, q4), ((u - 1) >> 2) & 1u, abort_v, a.status));
+            if (!alive) continue;
+            m_old = s_max[ps][qi];
+          }
+          // The maximum moves only when a sub-chunk exceeds it by more than 8 (log2 units): P stays below 2^8, most
+          // sub-chunks rescale nothing, and P, the sums and O share it.
+          const bool grow = mc > m_old + 8.f;
+          const float m_new = grow ? mc : m_old;
+          s_max[set][qi] = m_new;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(MAX(set, q4));
+          if (i > 0 && __any_sync(0xffffffffu, grow)) {
+            // O takes the new maximum between P V of the last sub-chunk (waited for; the one before on that buffer was
+            // over before this buffer's S) and of this one (after its P_FULL)
+            alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE((u - 1) & 3u), ((u - 1) >> 2) & 1u, abort_v, a.status));
+            if (!alive) continue;
+            tc_fence_after();
+            const float alpha = grow ? (m_old == -INFINITY ? 0.f : ex2a(m_old - m_new)) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < DP / 16; ++c) {
+              float ov[16];
+              tmem_ld16(o_tm + (uint32_t)(c * 16), ov);
 #pragma unroll
-        for (int c = 0; c < kPart / 2; ++c) {
-          const float p0 = ex2a(fmaf(__uint_as_float(sr[2 * c]), sc, -m_use));
-          const float p1 = ex2a(fmaf(__uint_as_float(sr[2 * c + 1]), sc, -m_use));
-          ps[c & 3] += p0 + p1;
-          sr[c] = packb(p0, p1);
+              for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+              tmem_st16(o_tm + (uint32_t)(c * 16), ov);
+            }
+          }
+          if (m_new != m_own) {
+            l_run *= m_own == -INFINITY ? 0.f : ex2a(m_own - m_new);
+            m_own = m_new;
+          }
+          const float m_use = m_new == -INFINITY ? 0.f : m_new;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+          // P: keys 32 .. 63 first (columns 48 .. 63 of the buffer), then keys 0 .. 31 (columns 32 .. 47)
+#pragma unroll
+          for (int hf = 1; hf >= 0; --hf) {
+            if (hf == 0) {
+              tmem_ld32_issue(s_tm, sr);
+              tmem_wait_ld_tie32(sr);
+              if (cut) mask32(sr, lo);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float p0 = ex2a(fmaf(__uint_as_float(sr[2 * c]), sc, -m_use));
+              const float p1 = ex2a(fmaf(__uint_as_float(sr[2 * c + 1]), sc, -m_use));
+              ps[c & 3] += p0 + p1;
+              sr[c] = packb(p0, p1);
+            }
+            tmem_st16u(s_tm + (uint32_t)(hf ? 48 : 32), sr);
+          }
+          l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        } else if (lane == 0) {
+          mbar_arrive(MAX(set, q4));  // (the phases count sub-chunks in every segment)
         }
-        // P: 16 columns over the upper half of this thread's own scores
-        tmem_st16u(s_buf + (uint32_t)(pt * kPart + 16), sr);
-        l_run = l_run * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
-        }
-        if (hb == 0 && (alone || t == 0) && sq.nk - key0 < kKC) {
-          // past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
-          // zeros; the rows are cleared after the copy and before P_FULL lets P V start.
-          alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(gj % kStages), (gj / kStages) & 1u, abort_v, a.status));
+        if (left < c0 + kSub) {
+          // Past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
+          // zeros; the rows of this sub-chunk are cleared after the copy and before P_FULL lets P V start.  (V's stage
+          // held the chunk kVStages before, whose P V was over before this buffer's S.)
+          alive = __all_sync(0xffffffffu,
+                             wait_bounded(V_FULL(gj % kVStages), (gj / kVStages) & 1u, abort_v, a.status));
           if (!alive) continue;
-          const int r0 = max(sq.nk - key0, 0), r1 = min(kKC, (r0 + box - 1) / box * box);
-          for (int w = st_id & (32 * kSoftWarps - 1); w < (r1 - r0) * (DP / 8); w += 32 * kSoftWarps)
-            *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kStages) * C::kTile +
+          const int nv = max(left, 0), r0 = max(nv, c0), r1 = min(c0 + kSub, (nv + box - 1) / box * box);
+          for (int w = qi; w < (r1 - r0) * (DP / 8); w += 128)
+            *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kVStages) * C::kTile +
                                        tile_off(r0 + w / (DP / 8), w % (DP / 8))) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
-          __syncwarp();
-          if (!alone && lane == 0) mbar_arrive(V_CLEAR);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(P_FULL(t, hb));
+        if (lane == 0) mbar_arrive(P_FULL(set));
       }
-      // ---- the segment's end
+      // ---- the segment's end: the sets' sums, and a quarter of O's columns for each
       if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
-      s_l[t][pt][qi] = l_run;
-      if (pt == 0) s_m[t][qi] = m_run;
+      s_ml[set][qi] = make_float2(m_own, l_run);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory");
       const bool starts = seg.blk == 0, ends = n == sq.nblk - seg.blk;
       const int slot = s0 == rg.u0 ? 0 : 1;
-      const size_t share = (size_t)blockIdx.x * 2 + slot;
-      // O columns of this thread, and its query: tiles of their own, half a row per thread; alone, the four threads of
-      // a row take a quarter each of both O's (fa, fb: their weights)
-      int q, c0, nc;
-      float m, l, fa = 1.f, fb = 0.f;
-      if (alone) {
-        asm volatile("bar.sync %0, 128;" ::"r"(9 + q4) : "memory");
-        const float ma = s_m[0][qi], mb = s_m[1][qi];
-        m = fmaxf(ma, mb);
-        fa = ma == -INFINITY ? 0.f : ex2a(ma - m);
-        fb = mb == -INFINITY ? 0.f : ex2a(mb - m);
-        l = (s_l[0][0][qi] + s_l[0][1][qi]) * fa + (s_l[1][0][qi] + s_l[1][1][qi]) * fb;
-        q = qi;
-        nc = DP / 4;
-        c0 = (2 * pt + t) * nc;
-      } else {
-        pair_sync();
-        m = m_run;
-        l = s_l[t][0][qi] + s_l[t][1][qi];
-        q = t * 128 + qi;
-        nc = DP / 2;
-        c0 = pt * nc;
-      }
-      if (alive) {
+      if (alive && used) {
         tc_fence_after();
-        bf16 *dst = static_cast<bf16 *>(a.out) + pairs.at(q < nq ? q : 0, seg.kvh, a.n_heads, hd);
-        float *po = part_o + share_at(share, R, DP, q, 0);
-        const float inv = starts && ends ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-        const uint32_t oa = tmem + C::kO + (alone ? 0u : 128u * t) + lane_off;
-#pragma unroll 1
-        for (int c = c0; c < c0 + nc; c += 16) {
-          float ov[16];
-          tmem_ld16(oa + (uint32_t)c, ov);
-          if (alone) {
-            float ob[16];
-            if (n > 1) tmem_ld16(oa + 128u + (uint32_t)c, ob);
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = n > 1 ? ov[e] * fa + ob[e] * fb : ov[e];
-          }
-          if (q < nq && c < hd) {
+        for (int s = 0; s < kSets; ++s) m = fmaxf(m, s_ml[s][qi].x);  // the maximum never falls: the last sub-chunk's
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+          const float2 ml = s_ml[s][qi];
+          l += ml.x == -INFINITY ? ml.y : ml.y * ex2a(ml.x - m);
+        }
+        const size_t share = (size_t)blockIdx.x * 2 + slot;
+        bf16 *dst = static_cast<bf16 *>(a.out) + pairs.at(qi < nq ? qi : 0, seg.kvh, a.n_heads, hd);
+        float *po = part_o + share_at(share, R, DP, qi, 0);
+        const float inv = starts && ends ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+#pragma unroll
+        for (int c = (int)set * (DP / 4); c < (int)set * (DP / 4) + DP / 4; c += 16) {
+          float ov[16];
+          tmem_ld16(o_tm + (uint32_t)c, ov);
+          if (qi < nq && c < hd) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) ov[e] *= inv;
             if (starts && ends) {
@@ -486,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (q < nq && c0 == 0 && !(starts && ends)) part_ml[share * R + q] = make_float2(m, l);
+        if (set == 0 && qi < nq && !(starts && ends)) part_ml[share * R + qi] = make_float2(m, l);
         tc_fence_before();
       }
       if (s1 == rg.u1 && st_id == 0) {
