@@ -7,10 +7,10 @@
 //               slots x 64 dims (128-byte swizzle), into a K and a V ring; a box
 //               past the sequence's end or on a bad page is read at a page
 //               coordinate outside the tensor, i.e. as zeros
-//   warp 1      MMA issuer (one elected thread): S_u = Q K_u^T (M = 128 queries,
-//               N = 64 keys) into one of four score buffers in tensor memory,
-//               three sub-chunks ahead, and O += P_u V_u (P_u in tensor memory,
-//               V MN-major)
+//   warps 1, 2  MMA issuers (one elected thread each): S_u = Q K_u^T (M = 128
+//               queries, N = 64 keys) into one of four score buffers in tensor
+//               memory, and O += P_u V_u (P_u in tensor memory, V MN-major); one
+//               warp for both spent 0.9 us a sub-chunk on waits and issues
 //   warps 4-19  softmax, four sets of four warps: set u % 4 takes sub-chunk u, a
 //               thread is a query and has all 64 keys
 //
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kSets + 3 + 4 * kSets];
+  __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kSets + 4 + 4 * kSets];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
@@ -114,8 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto S_FULL = [&](uint32_t b) { return bar1 + 8u * b; };                   // scores of buffer b are there
   auto P_FULL = [&](uint32_t b) { return bar1 + 8u * (kSets + b); };         // its P is there
   auto PV_DONE = [&](uint32_t b) { return bar1 + 8u * (2 * kSets + b); };    // its P V is in O
-  const uint32_t Q_FULL = bar1 + 8u * (3 * kSets), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;
-  auto MAX = [&](uint32_t set, int q4) { return Q_FULL + 24u + 8u * (set * 4u + (uint32_t)q4); };  // s_max[set] of 32 rows
+  const uint32_t Q_FULL = bar1 + 8u * (3 * kSets), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;  // DRAIN: two
+  auto MAX = [&](uint32_t set, int q4) { return Q_FULL + 32u + 8u * (set * 4u + (uint32_t)q4); };  // s_max[set] of 32 rows
 
   if (tid == 0) {
     for (uint32_t i = 0; i < 2 * (kKStages + kVStages); ++i) mbar_init(bar0 + 8u * i, 1);
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(Q_FULL, 4 * kSets);
     mbar_init(O_FINAL, 1);
     mbar_init(DRAIN, 1);
+    mbar_init(DRAIN + 8u, 1);
     abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&kmap);
@@ -203,76 +204,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t s = 0; s < kVStages; ++s)
         if (nv_ > s) wait_drain(V_FULL(s), ((nv_ - 1 - s) / kVStages) & 1u);
     }
-  } else if (warp == 1) {
-    // ---- MMA issuer: the warp runs as one, an elected lane issues
+  } else if (warp <= 2) {
+    // ---- MMA issuers: a warp runs as one, an elected lane issues
+    const bool pv = warp == 2;
     const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
     const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
     constexpr uint64_t kStep = C::kTile >> 4, kHalf = (uint64_t)(kSub * 128 >> 4);  // descriptor distances
     bool ok = true, any = false;
-    uint32_t g = 0, nseg = 0;  // chunks of the CTA before the segment, segments
+    uint32_t u = 0, nseg = 0;  // sub-chunks, segments
     auto wait = [&](uint32_t bar, uint32_t par) {
       ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
       return ok;
     };
-    // scores of sub-chunk i of the segment
-    auto issue_s = [&](int i) {
-      const uint32_t gj = g + (uint32_t)(i >> 1), st = gj % kKStages, h = (uint32_t)(i & 1), b = (2 * g + i) & 3u;
-      if (h == 0 && !wait(K_FULL(st), gj / kKStages)) return;
-      tc_fence_after();
-      const uint64_t kd = kd0 + st * kStep + h * kHalf;
-      if (elect_one()) {
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
-          tc_mma(tmem + b * 64u, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(S_FULL(b));
-        mbar_arrive(S_FULL(b));
-        if (h) tc_commit(K_EMPTY(st));
-      }
-      __syncwarp();
-      any = true;
-    };
     for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
       const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-      const int n = (int)(s1 - s0), ns = 2 * n;
-      if (!wait(Q_FULL, nseg)) break;
-      // Three sub-chunks ahead.  A buffer's last P V (of the segment before, or of sub-chunk i - 4) has been waited for.
-      for (int i = 0; i < min(3, ns) && ok; ++i) issue_s(i);
-      for (int i = 0; i < ns && ok; ++i) {
-        const uint32_t u = 2 * g + (uint32_t)i, b = u & 3u, gj = g + (uint32_t)(i >> 1), st = gj % kVStages;
-        if (!wait(P_FULL(b), u >> 2) || ((i & 1) == 0 && !wait(V_FULL(st), gj / kVStages))) break;
-        tc_fence_after();
-        const uint64_t vd = vd0 + st * kStep + (uint64_t)(i & 1) * kHalf;
-        if (elect_one()) {
+      const int ns = 2 * (int)(s1 - s0);
+      if (!pv) {
+        if (!wait(Q_FULL, nseg)) break;
+        for (int i = 0; i < ns; ++i, ++u) {
+          const uint32_t b = u & 3u, st = (u >> 1) % kKStages, h = u & 1u;
+          // the buffer's last P V has read its P
+          if ((h == 0 && !wait(K_FULL(st), (u >> 1) / kKStages)) || (u >= 4 && !wait(PV_DONE(b), (u >> 2) - 1u))) break;
+          tc_fence_after();
+          const uint64_t kd = kd0 + st * kStep + h * kHalf;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kSub / 16; ++kk)
-            tc_mma_ts(tmem + C::kO, tmem + b * 64u + 32u + (uint32_t)(kk * 8), vd + (uint64_t)(kk * (2048 >> 4)), id_o,
-                      (i > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(PV_DONE(b));
-          if (i & 1) tc_commit(V_EMPTY(st));
+            for (int kk = 0; kk < DP / 16; ++kk) {
+              const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
+              tc_mma(tmem + b * 64u, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(S_FULL(b));
+            mbar_arrive(S_FULL(b));
+            if (h) tc_commit(K_EMPTY(st));
+          }
+          __syncwarp();
+          any = true;
         }
-        __syncwarp();
-        if (i + 3 < ns) {
-          // the buffer of sub-chunk i + 3 is that of i - 1, whose P V must have read its P
-          if (i > 0 && !wait(PV_DONE((u - 1) & 3u), (u - 1) >> 2)) break;
-          issue_s(i + 3);
+      } else {
+        for (int i = 0; i < ns; ++i, ++u) {
+          const uint32_t b = u & 3u, st = (u >> 1) % kVStages, h = u & 1u;
+          if ((h == 0 && !wait(V_FULL(st), (u >> 1) / kVStages)) || !wait(P_FULL(b), u >> 2)) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + st * kStep + h * kHalf;
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kSub / 16; ++kk)
+              tc_mma_ts(tmem + C::kO, tmem + b * 64u + 32u + (uint32_t)(kk * 8), vd + (uint64_t)(kk * (2048 >> 4)), id_o,
+                        (i > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(PV_DONE(b));
+            if (h) tc_commit(V_EMPTY(st));
+            if (i == ns - 1) tc_commit(O_FINAL);
+          }
+          __syncwarp();
+          any = true;
         }
       }
       if (!ok) break;
-      // the last four P V of the segment: waited for in order, so that no PV_DONE wait falls a phase behind
-      for (int i = max(0, ns - 4); i < ns && ok; ++i) wait(PV_DONE((2 * g + i) & 3u), (2 * g + (uint32_t)i) >> 2);
-      if (!ok) break;
-      if (elect_one()) tc_commit(O_FINAL);
-      __syncwarp();
-      g += (uint32_t)n;
-      advance<R, kKC>(a, seg, n);
+      advance<R, kKC>(a, seg, ns / 2);
       s0 = s1;
     }
     if (!ok && any) {
-      if (elect_one()) tc_commit(DRAIN);
+      const uint32_t drain = DRAIN + (pv ? 8u : 0u);
+      if (elect_one()) tc_commit(drain);
       __syncwarp();
-      wait_drain(DRAIN, 0);
+      wait_drain(drain, 0);
     }
   } else if (warp >= kSoft0) {
     // ---- softmax
@@ -352,8 +347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(MAX(set, q4));
           if (i > 0 && __any_sync(0xffffffffu, grow)) {
-            // O takes the new maximum between P V of the last sub-chunk (waited for; the one before on that buffer was
-            // over before this buffer's S) and of this one (after its P_FULL)
+            // O takes the new maximum between P V of the last sub-chunk (waited for; the one before on that barrier was
+            // waited for by the issuer of this buffer's S) and of this one (after its P_FULL)
             alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE((u - 1) & 3u), ((u - 1) >> 2) & 1u, abort_v, a.status));
             if (!alive) continue;
             tc_fence_after();
