@@ -3,12 +3,12 @@
 // k_paged_attn.cu, with items of up to 128 queries (one TMEM lane each) and
 // units of 128 keys, worked in sub-chunks of 64:
 //
-//   warp 0      TMA producer: the pages of a chunk of 128 keys, boxes of `box`
-//               slots x 64 dims (128-byte swizzle), into a K and a V ring; a box
+//   warps 0, 3  TMA producers of K and of V: the pages of a sub-chunk, boxes of
+//               `box` slots x 64 dims (128-byte swizzle), into a ring each; a box
 //               past the sequence's end or on a bad page is read at a page
 //               coordinate outside the tensor, i.e. as zeros
 //   warps 1, 2  MMA issuers (one elected thread each): S_u = Q K_u^T (M = 128
-//               queries, N = 64 keys) into one of four score buffers in tensor
+//               queries, N = 64 keys) into one of six score buffers in tensor
 //               memory, and O += P_u V_u (P_u in tensor memory, V MN-major); one
 //               warp for both spent 0.9 us a sub-chunk on waits and issues
 //   warps 4-19  softmax, four sets of four warps: set u % 4 takes sub-chunk u, a
@@ -16,11 +16,11 @@
 //
 // The only thing that goes from one sub-chunk to the next is the running maximum
 // (O, P and the sums share it): a set waits for its predecessor's maximum, not
-// for its exponentials, so four sub-chunks are in work at a time and neither the
-// MMA's nor the softmax's latency is on the critical path.  (Two tiles of 128
+// for its exponentials, so four sub-chunks are in the softmax at a time, two more
+// in the MMAs, and neither's latency is on the critical path.  (Two tiles of 128
 // queries taking turns on two buffers each, measured before: 1.3 us per 128
 // queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
-// TMEM: four score buffers of 64 columns, O of head_dim columns; P (bf16 pairs)
+// TMEM: six score buffers of 64 columns, O of head_dim columns; P (bf16 pairs)
 // overwrites the second half of its scores, which are in registers by then.
 // P is rounded to bf16 once, as in the dense attention of a step: a second
 // product for the low part would cost half as much again on the tensor pipe.
@@ -37,22 +37,25 @@ namespace {
 
 constexpr int kKC = 128;              // keys of a unit
 constexpr int kSub = 64;              // keys of a sub-chunk
-constexpr int kKStages = 3, kVStages = 2;  // ring depths (chunks)
-constexpr int kSets = 4;              // softmax sets = score buffers
+constexpr uint32_t kKStages = 5, kVStages = 6;  // ring depths (sub-chunks)
+constexpr uint32_t kBufs = 6;         // score buffers
+constexpr uint32_t kSets = 4;         // softmax sets
 constexpr int kSoft0 = 4;             // first softmax warp
 constexpr int kWarps = kSoft0 + 4 * kSets;
 constexpr int kThreads = 32 * kWarps;
 
 template <int DP>
 struct TcCfg {
-  static constexpr uint32_t kTile = 128u * DP * 2u;  // the Q tile, or K or V of a chunk: DP / 64 blocks of 16 KB
-  static constexpr uint32_t kSmem = (1 + kKStages + kVStages) * kTile + 1024u;
+  static constexpr uint32_t kQ = 128u * DP * 2u;     // the Q tile: DP / 64 blocks of 128 rows x 128 bytes
+  static constexpr uint32_t kTile = 64u * DP * 2u;   // K or V of a sub-chunk: DP / 64 blocks of 64 rows x 128 bytes
+  static constexpr uint32_t kSmem = kQ + (kKStages + kVStages) * kTile + 1024u;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kO = 256;                // O at column 256
+  static constexpr uint32_t kO = 64 * kBufs;         // column of O
 };
 
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {  // 16-byte chunk c of row r
-  return (uint32_t)(c >> 3) * 16384u + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
+template <int ROWS>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {  // 16-byte chunk c of row r of a tile of ROWS rows
+  return (uint32_t)(c >> 3) * (uint32_t)(ROWS * 128) + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4);
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
                                         uint32_t bar) {
@@ -93,18 +96,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries;
   extern __shared__ uint8_t sm_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kSets + 4 + 4 * kSets];
+  __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kBufs + 4 + 4 * kSets];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ long long s_scan[kWarps];
   __shared__ Place s_place;
   __shared__ float s_max[kSets][128];   // [set] running maximum after the set's sub-chunk
   __shared__ float2 s_ml[kSets][128];   // [set] (maximum, sum) at the end of a segment
-  __shared__ uint32_t s_bad[8];         // [chunk % 8] boxes of the chunk on bad pages
+  __shared__ uint32_t s_bad[16];        // [sub-chunk % 16] its boxes on bad pages
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
-  const uint32_t q_s = sbase, k_s = sbase + C::kTile, v_s = k_s + kKStages * C::kTile;
+  const uint32_t q_s = sbase, k_s = sbase + C::kQ, v_s = k_s + kKStages * C::kTile;
   const uint32_t bar0 = smem_u32(bars);
   auto K_FULL = [&](uint32_t s) { return bar0 + 8u * s; };
   auto K_EMPTY = [&](uint32_t s) { return bar0 + 8u * (kKStages + s); };
@@ -112,19 +115,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto V_EMPTY = [&](uint32_t s) { return bar0 + 8u * (2 * kKStages + kVStages + s); };
   const uint32_t bar1 = bar0 + 8u * (2 * (kKStages + kVStages));
   auto S_FULL = [&](uint32_t b) { return bar1 + 8u * b; };                   // scores of buffer b are there
-  auto P_FULL = [&](uint32_t b) { return bar1 + 8u * (kSets + b); };         // its P is there
-  auto PV_DONE = [&](uint32_t b) { return bar1 + 8u * (2 * kSets + b); };    // its P V is in O
-  const uint32_t Q_FULL = bar1 + 8u * (3 * kSets), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;  // DRAIN: two
+  auto P_FULL = [&](uint32_t b) { return bar1 + 8u * (kBufs + b); };         // its P is there
+  auto PV_DONE = [&](uint32_t b) { return bar1 + 8u * (2 * kBufs + b); };    // its P V is in O
+  const uint32_t Q_FULL = bar1 + 8u * (3 * kBufs), O_FINAL = Q_FULL + 8u, DRAIN = Q_FULL + 16u;  // DRAIN: two
   auto MAX = [&](uint32_t set, int q4) { return Q_FULL + 32u + 8u * (set * 4u + (uint32_t)q4); };  // s_max[set] of 32 rows
 
   if (tid == 0) {
     for (uint32_t i = 0; i < 2 * (kKStages + kVStages); ++i) mbar_init(bar0 + 8u * i, 1);
-    for (uint32_t b = 0; b < kSets; ++b) {
-      mbar_init(S_FULL(b), 2);  // the scores (commit), and the issuer itself (it has seen the chunk's K_FULL)
+    for (uint32_t b = 0; b < kBufs; ++b) {
+      mbar_init(S_FULL(b), 2);  // the scores (commit), and the issuer itself (it has seen K_FULL, and so s_bad)
       mbar_init(P_FULL(b), 4);
       mbar_init(PV_DONE(b), 1);
-      for (int q = 0; q < 4; ++q) mbar_init(MAX(b, q), 1);
     }
+    for (uint32_t i = 0; i < 4 * kSets; ++i) mbar_init(MAX(0, 0) + 8u * i, 1);
     mbar_init(Q_FULL, 4 * kSets);
     mbar_init(O_FINAL, 1);
     mbar_init(DRAIN, 1);
@@ -150,68 +153,78 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (!rg.any) {
     if (tid == 0) shares[blockIdx.x].last = -1;
-  } else if (warp == 0) {
-    // ---- TMA producer
-    Place &ld = seg;
-    const int nb = kKC / box;                     // boxes of a chunk (of each 64-dim half)
-    const int my = lane % nb, half = lane / nb;   // the lane's box: lanes 0 .. nb * DP / 64 - 1 issue
-    const bool mine = half < DP / 64;
-    auto look = [&]() {
-      const int key = ld.blk * kKC + my * box;
-      return mine && key < ld.s.nk ? a.table[(size_t)ld.b * a.max_pages + div_page(a, (unsigned)key)] : -1;
+  } else if (warp == 0 || warp == 3) {
+    // ---- TMA producers
+    const bool is_v = warp == 3;
+    const uint32_t stages = is_v ? kVStages : kKStages, ring = is_v ? v_s : k_s;
+    const uint32_t full0 = is_v ? V_FULL(0) : K_FULL(0), empty0 = is_v ? V_EMPTY(0) : K_EMPTY(0);
+    const CUtensorMap *map = is_v ? &vmap : &kmap;
+    const int nb = kSub / box;                    // boxes of a sub-chunk (of each 64-dim block)
+    const int my = lane % nb, blk = lane / nb;    // the lane's box: lanes 0 .. nb * DP / 64 - 1 issue
+    const bool mine = blk < DP / 64;
+    const uint32_t dst = (uint32_t)blk * (uint32_t)(kSub * 128) + (uint32_t)(my * box) * 128u;
+    // first key of the lane's box in sub-chunk h of the place, and its page (-1: none), looked up one ahead
+    auto key_of = [&](uint32_t h) { return seg.blk * kKC + (int)h * kSub + my * box; };
+    auto look = [&](uint32_t h) {
+      const int key = key_of(h);
+      return mine && key < seg.s.nk ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)] : -1;
     };
-    int pg = look();
-    uint32_t g = 0, nk_ = 0, nv_ = 0;  // chunk of the CTA; K and V copies issued
+    int pg = look(0);
+    uint32_t st = 0, par = 1, u = 0;  // stage, its EMPTY parity, sub-chunk
     bool ok = true;
-    for (long long u = rg.u0; u < rg.u1 && ok; ++u, ++g) {
-      const int key = ld.blk * kKC + my * box, kvh = ld.kvh;
-      const bool in = mine && key < ld.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
-      if (in && !good && half == 0 && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
-      const uint32_t bad = __ballot_sync(0xffffffffu, in && !good) & ((1u << nb) - 1u);  // lanes of half 0
+    for (long long left = 2 * (rg.u1 - rg.u0); left > 0; --left, ++u) {
+      const int key = key_of(u & 1u), kvh = seg.kvh;
+      const bool in = mine && key < seg.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
+      const uint32_t bad = __ballot_sync(0xffffffffu, in && !good) & ((1u << nb) - 1u);  // lanes of block 0
       const int w = good ? pg : a.pages.n_pages;  // outside the tensor: zeros
       const int y = good ? key - (int)(div_page(a, (unsigned)key) * (unsigned)a.pages.page_size) : 0;
-      const int c1 = head_first ? kvh : y, c2 = head_first ? y : kvh;
-      const uint32_t dst = (uint32_t)half * 16384u + (uint32_t)(my * box) * 128u;
-      if (u + 1 < rg.u1) {
-        advance<R, kKC>(a, ld, 1);
-        pg = look();
+      if (left > 1) {
+        if (u & 1u) advance<R, kKC>(a, seg, 1);
+        pg = look((u + 1) & 1u);
       }
-      {
-        const uint32_t st = g % kKStages;
-        ok = __all_sync(0xffffffffu, wait_bounded(K_EMPTY(st), ((g / kKStages) & 1u) ^ 1u, abort_v, a.status));
-        if (!ok) break;
-        if (lane == 0) {
-          s_bad[g & 7u] = bad;  // read by the softmax with the scores of the chunk; eight chunks later all have
-          mbar_expect_tx(K_FULL(st), C::kTile);
+      ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8u * st, par, abort_v, a.status));
+      if (!ok) break;
+      if (lane == 0) {
+        if (!is_v) {
+          s_bad[u & 15u] = bad;  // read by the softmax with the scores; sixteen sub-chunks later it has been
+          if (bad && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
         }
-        __syncwarp();
-        if (mine) tma_box(k_s + st * C::kTile + dst, &kmap, half * 64, c1, c2, w, K_FULL(st));
-        ++nk_;
+        mbar_expect_tx(full0 + 8u * st, C::kTile);
       }
-      {
-        const uint32_t st = g % kVStages;
-        ok = __all_sync(0xffffffffu, wait_bounded(V_EMPTY(st), ((g / kVStages) & 1u) ^ 1u, abort_v, a.status));
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(V_FULL(st), C::kTile);
-        __syncwarp();
-        if (mine) tma_box(v_s + st * C::kTile + dst, &vmap, half * 64, c1, c2, w, V_FULL(st));
-        ++nv_;
+      __syncwarp();
+      if (mine)
+        tma_box(ring + st * C::kTile + dst, map, blk * 64, head_first ? kvh : y, head_first ? y : kvh, w,
+                full0 + 8u * st);
+      if (++st == stages) {
+        st = 0;
+        par ^= 1u;
       }
     }
-    if (!ok) {  // wait, bounded, for the copies still in flight: the last phase of every stage
-      for (uint32_t s = 0; s < kKStages; ++s)
-        if (nk_ > s) wait_drain(K_FULL(s), ((nk_ - 1 - s) / kKStages) & 1u);
-      for (uint32_t s = 0; s < kVStages; ++s)
-        if (nv_ > s) wait_drain(V_FULL(s), ((nv_ - 1 - s) / kVStages) & 1u);
-    }
+    if (!ok)  // wait, bounded, for the copies still in flight: the last phase of every stage
+      for (uint32_t s = 0; s < stages; ++s)
+        if (u > s) wait_drain(full0 + 8u * s, ((u - 1 - s) / stages) & 1u);
   } else if (warp <= 2) {
     // ---- MMA issuers: a warp runs as one, an elected lane issues
     const bool pv = warp == 2;
     const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
-    const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, 16384u);
-    constexpr uint64_t kStep = C::kTile >> 4, kHalf = (uint64_t)(kSub * 128 >> 4);  // descriptor distances
+    const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, kSub * 128u);
+    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
     bool ok = true, any = false;
-    uint32_t u = 0, nseg = 0;  // sub-chunks, segments
+    uint32_t nseg = 0;                                        // segments
+    uint32_t st = 0, st_par = 0, b = 0, b_par = 0;            // stage and buffer of the sub-chunk, their FULL parities
+    const uint32_t stages = pv ? kVStages : kKStages;
+    bool fresh = true;                                        // the buffers have not been used yet
+    auto step = [&]() {
+      if (++st == stages) {
+        st = 0;
+        st_par ^= 1u;
+      }
+      if (++b == kBufs) {
+        b = 0;
+        b_par ^= 1u;
+        fresh = false;
+      }
+    };
     auto wait = [&](uint32_t bar, uint32_t par) {
       ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
       return ok;
@@ -221,38 +234,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int ns = 2 * (int)(s1 - s0);
       if (!pv) {
         if (!wait(Q_FULL, nseg)) break;
-        for (int i = 0; i < ns; ++i, ++u) {
-          const uint32_t b = u & 3u, st = (u >> 1) % kKStages, h = u & 1u;
+        for (int i = 0; i < ns; ++i, step()) {
           // the buffer's last P V has read its P
-          if ((h == 0 && !wait(K_FULL(st), (u >> 1) / kKStages)) || (u >= 4 && !wait(PV_DONE(b), (u >> 2) - 1u))) break;
+          if (!wait(K_FULL(st), st_par) || (!fresh && !wait(PV_DONE(b), b_par ^ 1u))) break;
           tc_fence_after();
-          const uint64_t kd = kd0 + st * kStep + h * kHalf;
+          const uint64_t kd = kd0 + st * kStep;
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3));
-              tc_mma(tmem + b * 64u, qd + off, kd + off, id_s, kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < DP / 16; ++kk)
+              tc_mma(tmem + b * 64u, qd + (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3)),
+                     kd + (uint64_t)((kk >> 2) * (kSub * 128 >> 4) + 2 * (kk & 3)), id_s, kk > 0 ? 1u : 0u);
             tc_commit(S_FULL(b));
             mbar_arrive(S_FULL(b));
-            if (h) tc_commit(K_EMPTY(st));
+            tc_commit(K_EMPTY(st));
           }
           __syncwarp();
           any = true;
         }
       } else {
-        for (int i = 0; i < ns; ++i, ++u) {
-          const uint32_t b = u & 3u, st = (u >> 1) % kVStages, h = u & 1u;
-          if ((h == 0 && !wait(V_FULL(st), (u >> 1) / kVStages)) || !wait(P_FULL(b), u >> 2)) break;
+        for (int i = 0; i < ns; ++i, step()) {
+          if (!wait(V_FULL(st), st_par) || !wait(P_FULL(b), b_par)) break;
           tc_fence_after();
-          const uint64_t vd = vd0 + st * kStep + h * kHalf;
+          const uint64_t vd = vd0 + st * kStep;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kSub / 16; ++kk)
               tc_mma_ts(tmem + C::kO, tmem + b * 64u + 32u + (uint32_t)(kk * 8), vd + (uint64_t)(kk * (2048 >> 4)), id_o,
                         (i > 0 || kk > 0) ? 1u : 0u);
             tc_commit(PV_DONE(b));
-            if (h) tc_commit(V_EMPTY(st));
+            tc_commit(V_EMPTY(st));
             if (i == ns - 1) tc_commit(O_FINAL);
           }
           __syncwarp();
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t set = (uint32_t)(warp - kSoft0) / 4u;
     const int q4 = warp & 3, qi = q4 * 32 + lane;        // query of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-    const uint32_t s_tm = tmem + set * 64u + lane_off, o_tm = tmem + C::kO + lane_off;
+    const uint32_t o_tm = tmem + C::kO + lane_off;
     const int st_id = tid - 32 * kSoft0;
     const float sc = a.scale_log2;
     uint32_t g = 0, nseg = 0;  // chunks of the CTA before the segment, segments
@@ -287,10 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Pairs pairs(sq, q0, G);
       // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read theirs
       // (O_FINAL)
-      for (int i = st_id; i < 128 * (DP / 8); i += 128 * kSets) {
+      for (int i = st_id; i < 128 * (DP / 8); i += 128 * (int)kSets) {
         const int r = i / (DP / 8), c = i - r * (DP / 8);
         const bool in = r < nq && c * 8 < hd;
-        load_query16(q_s + tile_off(r, c),
+        load_query16(q_s + tile_off<128>(r, c),
                      static_cast<const bf16 *>(a.q) + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0),
                      in);
       }
@@ -300,23 +310,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(Q_FULL);
       const bool used = q4 * 32 < nq;             // this warp has queries
       float m_own = -INFINITY, l_run = 0.f;       // the maximum of this set's last sub-chunk, its share of the sum
-      for (int i = (int)((set - 2 * g) & 3u); i < ns; i += kSets) {
-        const uint32_t u = 2 * g + (uint32_t)i, gj = g + (uint32_t)(i >> 1);
-        const int c0 = (i & 1) * kSub;                           // the sub-chunk's first key in the chunk
-        const int left = sq.nk - (seg.blk + (i >> 1)) * kKC;     // keys of the sequence from the chunk's first on
-        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(set), (u >> 2) & 1u, abort_v, a.status));
+      for (int i = (int)((set - 2 * g) & 3u); i < ns; i += (int)kSets) {
+        const uint32_t u = 2 * g + (uint32_t)i, b = u % kBufs, s_tm = tmem + b * 64u + lane_off;
+        const int left = sq.nk - seg.blk * kKC - i * kSub;  // keys of the sequence from the sub-chunk's first on
+        // (a buffer's phase before this one is long over: the set that had it has handed its maximum down to this one)
+        if (alive) alive = __all_sync(0xffffffffu, wait_bounded(S_FULL(b), (u / kBufs) & 1u, abort_v, a.status));
         if (!alive) continue;  // nothing is handed on any more: every wait now fails
+        if (i > 0 && !used) {
+          alive = __all_sync(0xffffffffu, wait_bounded(MAX((set + 3u) & 3u, q4), ((u - 1) >> 2) & 1u, abort_v, a.status));
+          if (!alive) continue;
+        }
         if (used) {
           tc_fence_after();
           // Raw scores: the scale (> 0) commutes with the maximum and enters the exponent.  The first 32 keys are read
           // again for the exponentials rather than kept, which holds the thread within its registers.
           uint32_t lo = ~0u, hi = ~0u;  // valid keys
-          const uint32_t bad = s_bad[gj & 7u];
-          const bool cut = left < c0 + kSub || bad;
+          const uint32_t bad = s_bad[u & 15u];
+          const bool cut = left < kSub || bad;
           if (cut) {
-            unsigned long long v = left >= c0 + kSub ? ~0ull : left <= c0 ? 0ull : (1ull << (left - c0)) - 1ull;
+            unsigned long long v = left >= kSub ? ~0ull : left <= 0 ? 0ull : (1ull << left) - 1ull;
             for (int x = 0; x < kSub; x += box)
-              if ((bad >> ((c0 + x) / box)) & 1u) v &= ~((box >= kSub ? ~0ull : (1ull << box) - 1ull) << x);
+              if ((bad >> (x / box)) & 1u) v &= ~((box >= kSub ? ~0ull : (1ull << box) - 1ull) << x);
             lo = (uint32_t)v;
             hi = (uint32_t)(v >> 32);
           }
@@ -349,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i > 0 && __any_sync(0xffffffffu, grow)) {
             // O takes the new maximum between P V of the last sub-chunk (waited for; the one before on that barrier was
             // waited for by the issuer of this buffer's S) and of this one (after its P_FULL)
-            alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE((u - 1) & 3u), ((u - 1) >> 2) & 1u, abort_v, a.status));
+            alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE((u - 1) % kBufs), ((u - 1) / kBufs) & 1u, abort_v, a.status));
             if (!alive) continue;
             tc_fence_after();
             const float alpha = grow ? (m_old == -INFINITY ? 0.f : ex2a(m_old - m_new)) : 1.f;
@@ -389,23 +403,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (lane == 0) {
           mbar_arrive(MAX(set, q4));  // (the phases count sub-chunks in every segment)
         }
-        if (left < c0 + kSub) {
+        if (left < kSub) {
           // Past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
-          // zeros; the rows of this sub-chunk are cleared after the copy and before P_FULL lets P V start.  (V's stage
-          // held the chunk kVStages before, whose P V was over before this buffer's S.)
-          alive = __all_sync(0xffffffffu,
-                             wait_bounded(V_FULL(gj % kVStages), (gj / kVStages) & 1u, abort_v, a.status));
+          // zeros; the rest of the last box is cleared after the copy and before P_FULL lets P V start.  (The stage held
+          // sub-chunk u - kVStages, whose P V was waited for by the issuer of this buffer's S.)
+          const uint32_t st = u % kVStages;
+          static_assert(kVStages == kBufs, "the issuer of S_u has waited for P V of sub-chunk u - kBufs");
+          alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(st), (u / kVStages) & 1u, abort_v, a.status));
           if (!alive) continue;
-          const int nv = max(left, 0), r0 = max(nv, c0), r1 = min(c0 + kSub, (nv + box - 1) / box * box);
+          const int r0 = max(left, 0), r1 = (r0 + box - 1) / box * box;
           for (int w = qi; w < (r1 - r0) * (DP / 8); w += 128)
-            *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + (gj % kVStages) * C::kTile +
-                                       tile_off(r0 + w / (DP / 8), w % (DP / 8))) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(sm + (v_s - sbase) + st * C::kTile +
+                                       tile_off<kSub>(r0 + w / (DP / 8), w % (DP / 8))) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(P_FULL(set));
+        if (lane == 0) mbar_arrive(P_FULL(b));
       }
       // ---- the segment's end: the sets' sums, and a quarter of O's columns for each
       if (alive) alive = __all_sync(0xffffffffu, wait_bounded(O_FINAL, nseg & 1u, abort_v, a.status));
@@ -417,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int s = 0; s < kSets; ++s) m = fmaxf(m, s_ml[s][qi].x);  // the maximum never falls: the last sub-chunk's
+        for (uint32_t s = 0; s < kSets; ++s) m = fmaxf(m, s_ml[s][qi].x);  // the maximum never falls: the last sub-chunk's
 #pragma unroll
-        for (int s = 0; s < kSets; ++s) {
+        for (uint32_t s = 0; s < kSets; ++s) {
           const float2 ml = s_ml[s][qi];
           l += ml.x == -INFINITY ? ml.y : ml.y * ex2a(ml.x - m);
         }
@@ -491,7 +506,7 @@ cudaError_t launch_dp(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaS
 
 int tc_box_keys(const dcu_pages &p) {
   int box = 16;
-  while (box < 128 && p.page_size % (2 * box) == 0) box *= 2;
+  while (box < kSub && p.page_size % (2 * box) == 0) box *= 2;
   return box;
 }
 
