@@ -889,14 +889,6 @@ cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const S
                                                             : go(k_paged_merge<256, bf16>);
 }
 
-// Queries per sequence and kv head, on average, above which the tcgen05 kernel
-// is taken.  Measured, this kernel / that one: 1 x 1024 keys, 32 heads x 128:
-// 16 queries 16.3 / 16.1 us, 32 queries 20.4 / 17.2; 1 x 8192 keys: 16 queries
-// 54.2 / 54.6, 32 queries 68.3 / 56.3; 64 x 2000 keys of 28/4 heads: 14 queries
-// 94 / 113, 28 queries 115 / 113; 128 x 100 keys, 8 heads x 64: 16 queries
-// 44 / 52, 32 queries 60 / 55.
-constexpr long long kTcMinQueries = 24;
-
 int64_t paged_attention_workspace(const dcu_pages &p) {
   const int dp = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
   if (p.dtype == DCU_F32) return ShareBuf::bytes(8, dp);
@@ -908,17 +900,19 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
   if (a.pages.dtype == DCU_F32)
     return hd <= 64 ? launch<64, true, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, true, 1>(a, ws, s) : launch<256, true, 1>(a, ws, s);
-  // queries per sequence and kv head, on average (max_rows bounds the rows)
-  const long long queries = (long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads);
-  if (queries <= 8ll * a.B)
+  // Queries per sequence and kv head, on average (max_rows bounds the rows).  Up to 8 fill one mma.sync group; above,
+  // the tcgen05 kernel where it applies.  Measured, this kernel / that one, us a call: 1 x 1024 keys, 32 heads x 128:
+  // 1 query 11.6 / 14.0, 9 queries 16.2 / 13.9; 1 x 8192 keys: 8 queries 32.7 / 35.4, 16 queries 54.1 / 36.3; 64 x
+  // 2000 keys, 28/4 heads: 14 queries 93 / 65; 128 x 100 keys, 8 heads x 64: 8 queries 30.6 / 39.8, 16 queries
+  // 43.4 / 40.7.
+  if ((long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
-  PageMaps m;
-  if (queries > kTcMinQueries * a.B && a.scale_log2 > 0.f && hd <= 128 && a.pages.page_size % 16 == 0 &&
-      page_maps(a.pages, tc_box_keys(a.pages), &m))
+  if (hd > 128) return launch<256, false, 2>(a, ws, s);
+  PageMaps m = {};
+  if (a.scale_log2 > 0.f && a.pages.page_size % 16 == 0 && page_maps(a.pages, tc_box_keys(a.pages), &m))
     return launch_paged_attention_tc(a, m, ws, s);
-  return hd <= 64 ? launch<64, false, 4>(a, ws, s)
-                  : hd <= 128 ? launch<128, false, 4>(a, ws, s) : launch<256, false, 2>(a, ws, s);
+  return hd <= 64 ? launch_variant<64, false, 4, false>(a, m, ws, s) : launch_variant<128, false, 4, false>(a, m, ws, s);
 }
 
 }  // namespace dcu
