@@ -132,10 +132,11 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
   constexpr uint32_t FULL = (1u << KB) - 1u;
   pdl_enter();
   extern __shared__ uint8_t sm_raw[];
-  __shared__ long long s_scan[W];
+  __shared__ long long s_scan[2 * W];
   __shared__ Place s_place;
   __shared__ uint32_t s_mask[W][NST];
   __shared__ float2 s_ml[W][R];
+  __shared__ float2 s_fin[R];  // joined (max, sum) of a query
   __shared__ __align__(8) uint64_t s_bar[W][NST];
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -537,6 +538,17 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
         if (g == 0) s_ml[warp][n * 8 + 2 * t + c] = make_float2(m_run[n][c], l);
       }
     __syncthreads();
+    if (tid < ngrp * 8) {
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int w2 = 0; w2 < W; ++w2) M = fmaxf(M, s_ml[w2][tid].x);
+#pragma unroll
+      for (int w2 = 0; w2 < W; ++w2) {
+        const float2 ml = s_ml[w2][tid];
+        L += ml.x == -INFINITY ? ml.y : ml.y * exp2f(ml.x - M);  // (a sum without a maximum: 0, or NaN)
+      }
+      s_fin[tid] = make_float2(M, L);
+    }
     const int slot = s0 == u0 ? 0 : 1;  // the range's first segment, or its last one
     const size_t share = (size_t)blockIdx.x * 2 + slot;
 #pragma unroll
@@ -575,7 +587,7 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
 #pragma unroll
         for (int half = 1; half >= 0; --half) {
           if ((warp >= W / 2) == (half == 1)) {
-            float *bw = red + (size_t)(warp % (W / 2)) * DP * 8;  // [dim][8 queries]
+            float *bw = red + (size_t)(warp % (W / 2)) * DP * 8;  // [dim][8 queries], float32: [8 queries][dim]
             if constexpr (!F32) {
 #pragma unroll
               for (int i = 0; i < DP / 16; ++i)
@@ -594,24 +606,23 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
               constexpr int ND = C::kND;
               if (DP != 64 || lane < 16) {
 #pragma unroll
-                for (int i = 0; i < ND; ++i)
+                for (int r = 0; r < 8; ++r) {
+                  if (r >= nq) break;
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    float4 *d = reinterpret_cast<float4 *>(bw + ((lane + 32 * i) * 4 + e) * 8);
-#pragma unroll
-                    for (int r4 = 0; r4 < 2; ++r4) {
-                      float4 v = make_float4(o[0][(4 * r4) * ND + i][e], o[0][(4 * r4 + 1) * ND + i][e],
-                                             o[0][(4 * r4 + 2) * ND + i][e], o[0][(4 * r4 + 3) * ND + i][e]);
-                      if (half == 0) {
-                        const float4 w2 = d[r4];
-                        v.x += w2.x;
-                        v.y += w2.y;
-                        v.z += w2.z;
-                        v.w += w2.w;
-                      }
-                      d[r4] = v;
+                  for (int i = 0; i < ND; ++i) {
+                    float4 *d = reinterpret_cast<float4 *>(bw + r * DP + (lane + 32 * i) * 4);
+                    const float(&x)[4] = o[0][r * ND + i];
+                    float4 v = make_float4(x[0], x[1], x[2], x[3]);
+                    if (half == 0) {
+                      const float4 w2 = *d;
+                      v.x += w2.x;
+                      v.y += w2.y;
+                      v.z += w2.z;
+                      v.w += w2.w;
                     }
+                    *d = v;
                   }
+                }
               }
             }
           }
@@ -619,22 +630,16 @@ __global__ void __launch_bounds__(Cfg<DP, F32, NT>::kThreads, 1)
         }
         // sum of the W / 2 buffers: whole items are normalised and stored, cut ones go to the workspace
         for (int i = tid; i < DP * 8 / 2; i += C::kThreads) {
-          const int qr = i & 7, d = (i >> 3) * 2;
+          const int qr = F32 ? i / (DP / 2) : i & 7, d = (F32 ? i % (DP / 2) : i >> 3) * 2;
           if (n * 8 + qr >= nq || d >= hd) continue;
           float x0 = 0.f, x1 = 0.f;
 #pragma unroll
           for (int w2 = 0; w2 < W / 2; ++w2) {
-            x0 += red[(size_t)w2 * DP * 8 + d * 8 + qr];
-            x1 += red[(size_t)w2 * DP * 8 + (d + 1) * 8 + qr];
+            const float *x = red + (size_t)w2 * DP * 8 + (F32 ? qr * DP + d : d * 8 + qr);
+            x0 += x[0];
+            x1 += x[F32 ? 1 : 8];
           }
-          float M = -INFINITY, L = 0.f;
-#pragma unroll
-          for (int w2 = 0; w2 < W; ++w2) M = fmaxf(M, s_ml[w2][n * 8 + qr].x);
-#pragma unroll
-          for (int w2 = 0; w2 < W; ++w2) {
-            const float2 ml = s_ml[w2][n * 8 + qr];
-            L += ml.x == -INFINITY ? 0.f : ml.y * exp2f(ml.x - M);
-          }
+          const float M = s_fin[n * 8 + qr].x, L = s_fin[n * 8 + qr].y;
           if (starts && ends) {
             const float inv = L > 0.f || L != L ? 1.f / L : 0.f;
             const size_t at = pairs.at(n * 8 + qr, seg.kvh, a.n_heads, hd) + d;

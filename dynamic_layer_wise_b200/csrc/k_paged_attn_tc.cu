@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kBufs + 4 + 4 * kSets];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ long long s_scan[kWarps];
+  __shared__ long long s_scan[2 * kWarps];
   __shared__ Place s_place;
   __shared__ float s_max[kSets][128];   // [set] running maximum after the set's sub-chunk
   __shared__ float2 s_ml[kSets][128];   // [set] (maximum, sum) at the end of a segment

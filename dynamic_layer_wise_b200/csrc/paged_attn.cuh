@@ -121,7 +121,9 @@ __device__ __forceinline__ void locate(Place &p, long long off) {
 }
 
 // All W warps of the CTA: its range, and its first place in `first`.  A launch
-// uses as many ranges as have at least `least` units each (the grid at most).
+// uses the whole grid unless that leaves a range less than `least` units of an
+// item that is cut: as many ranges as there are items, or as many as have
+// `least` units, whichever is more.
 template <int R, int KB, int W>
 __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first, Place *place, long long *scan,
                                             int least) {
@@ -132,9 +134,9 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
     p.b = 0;
     p.s = seq_of<R, KB>(a, 0);
     const long long total = p.s.units(KV);
-    const int ranges = (int)min((long long)gridDim.x, div_ll(total + least - 1, least));
-    cut_even(rg, total, ranges);
     const long long items = (long long)KV * p.s.tiles;
+    const int ranges = (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least)));
+    cut_even(rg, total, ranges);
     if (total > 0 && items <= ranges) {
       // cut item by item when that adds no more to the longest range than `least` units, which a second item would cost
       const int f = ranges / (int)items;
@@ -155,12 +157,13 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + 32 * W - 1) / (32 * W);
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long long mine = 0;
+  long long mine = 0, items = 0;
   Place p;  // with one sequence per thread (B <= 32 W) its items are kept
   p.b = b0;
   for (int b = b0; b < b1; ++b) {
     p.s = seq_of<R, KB>(a, b);
     mine += p.s.units(KV);
+    items += (long long)KV * p.s.tiles;
   }
   long long x = mine;
 #pragma unroll
@@ -168,15 +171,22 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) scan[warp] = x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+  if (lane == 31) {
+    scan[warp] = x;
+    scan[W + warp] = items;
+  }
   __syncthreads();
   long long base = 0, total = 0;
+  items = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
     if (i == warp) base = total;
     total += scan[i];
+    items += scan[W + i];
   }
-  cut_even(rg, total, (int)min((long long)gridDim.x, div_ll(total + least - 1, least)));
+  cut_even(rg, total, (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least))));
   long long at = base + x - mine;
   if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
     if (per > 1)
