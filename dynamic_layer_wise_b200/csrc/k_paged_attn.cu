@@ -897,7 +897,7 @@ cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const S
 int64_t paged_attention_workspace(const dcu_pages &p) {
   const int dp = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
   if (p.dtype == DCU_F32) return ShareBuf::bytes(8, dp);
-  return dp == 256 ? ShareBuf::bytes(16, dp) : ShareBuf::bytes(kTcQueries, dp);
+  return ShareBuf::bytes(kTcQueries, dp);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_t s) {
@@ -913,11 +913,12 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
   if ((long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
-  if (hd > 128) return launch<256, false, 2>(a, ws, s);
   PageMaps m = {};
   if (a.scale_log2 > 0.f && a.pages.page_size % 16 == 0 && page_maps(a.pages, tc_box_keys(a.pages), &m))
     return launch_paged_attention_tc(a, m, ws, s);
-  return hd <= 64 ? launch_variant<64, false, 4, false>(a, m, ws, s) : launch_variant<128, false, 4, false>(a, m, ws, s);
+  return hd <= 64 ? launch_variant<64, false, 4, false>(a, m, ws, s)
+                  : hd <= 128 ? launch_variant<128, false, 4, false>(a, m, ws, s)
+                              : launch_variant<256, false, 2, false>(a, m, ws, s);
 }
 
 }  // namespace dcu

@@ -1,5 +1,5 @@
 // Paged attention of many query rows per sequence on the 5th-gen tensor cores
-// (bf16, head_dim up to 128).  Same line of work, shares and merge as
+// (bf16).  Same line of work, shares and merge as
 // k_paged_attn.cu, with items of up to 128 queries (one TMEM lane each) and
 // units of 128 keys, worked in sub-chunks of 64:
 //
@@ -20,7 +20,8 @@
 // in the MMAs, and neither's latency is on the critical path.  (Two tiles of 128
 // queries taking turns on two buffers each, measured before: 1.3 us per 128
 // queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
-// TMEM: six score buffers of 64 columns, O of head_dim columns; P (bf16 pairs)
+// TMEM: six score buffers of 64 columns, O of head_dim columns (head_dim above
+// 128: four buffers); P (bf16 pairs)
 // overwrites the second half of its scores, which are in registers by then.
 // P is rounded to bf16 once, as in the dense attention of a step: a second
 // product for the low part would cost half as much again on the tensor pipe.
@@ -37,8 +38,6 @@ namespace {
 
 constexpr int kKC = 128;              // keys of a unit
 constexpr int kSub = 64;              // keys of a sub-chunk
-constexpr uint32_t kKStages = 5, kVStages = 6;  // ring depths (sub-chunks)
-constexpr uint32_t kBufs = 6;         // score buffers
 constexpr uint32_t kSets = 4;         // softmax sets
 constexpr int kSoft0 = 4;             // first softmax warp
 constexpr int kWarps = kSoft0 + 4 * kSets;
@@ -48,6 +47,8 @@ template <int DP>
 struct TcCfg {
   static constexpr uint32_t kQ = 128u * DP * 2u;     // the Q tile: DP / 64 blocks of 128 rows x 128 bytes
   static constexpr uint32_t kTile = 64u * DP * 2u;   // K or V of a sub-chunk: DP / 64 blocks of 64 rows x 128 bytes
+  // ring depths (sub-chunks) and score buffers: what shared memory (227 KB) and tensor memory (512 columns) hold
+  static constexpr uint32_t kKStages = DP == 256 ? 2 : 5, kVStages = DP == 256 ? 2 : 6, kBufs = DP == 256 ? 4 : 6;
   static constexpr uint32_t kSmem = kQ + (kKStages + kVStages) * kTile + 1024u;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kO = 64 * kBufs;         // column of O
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float2 *__restrict__ part_ml, Share *__restrict__ shares) {
   using C = TcCfg<DP>;
   constexpr int R = kTcQueries;
+  constexpr uint32_t kKStages = C::kKStages, kVStages = C::kVStages, kBufs = C::kBufs;
   extern __shared__ uint8_t sm_raw[];
   __shared__ __align__(8) uint64_t bars[2 * (kKStages + kVStages) + 3 * kBufs + 4 + 4 * kSets];
   __shared__ uint32_t tmem_slot;
@@ -406,9 +408,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (left < kSub) {
           // Past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
           // zeros; the rest of the last box is cleared after the copy and before P_FULL lets P V start.  (The stage held
-          // sub-chunk u - kVStages, whose P V was waited for by the issuer of this buffer's S.)
-          const uint32_t st = u % kVStages;
-          static_assert(kVStages == kBufs, "the issuer of S_u has waited for P V of sub-chunk u - kBufs");
+          // sub-chunk u - kVStages, whose P V was waited for by the issuer of this buffer's S, or here.)
+          const uint32_t st = u % kVStages, before = u - kVStages;
+          static_assert(kVStages <= kBufs, "the issuer of S_u has waited for P V of sub-chunk u - kBufs");
+          if (kVStages < kBufs && u >= kVStages) {
+            alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE(before % kBufs), (before / kBufs) & 1u, abort_v, a.status));
+            if (!alive) continue;
+          }
           alive = __all_sync(0xffffffffu, wait_bounded(V_FULL(st), (u / kVStages) & 1u, abort_v, a.status));
           if (!alive) continue;
           const int r0 = max(left, 0), r1 = (r0 + box - 1) / box * box;
@@ -511,7 +517,8 @@ int tc_box_keys(const dcu_pages &p) {
 }
 
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s) {
-  return a.pages.head_dim <= 64 ? launch_dp<64>(a, m, ws, s) : launch_dp<128>(a, m, ws, s);
+  return a.pages.head_dim <= 64 ? launch_dp<64>(a, m, ws, s)
+                                : a.pages.head_dim <= 128 ? launch_dp<128>(a, m, ws, s) : launch_dp<256>(a, m, ws, s);
 }
 
 }  // namespace dcu

@@ -240,7 +240,7 @@ def case_inputs(seed, dtype, H, KV, hd, page, layout, lens, rows, tail=2, q_scal
 
 def check_attention(got, q, start, lens, table, k, v, dtype, scale):
     hd = q.shape[-1]
-    many = dtype == "bf16" and hd <= 128 and q.shape[0] * (q.shape[1] // k.shape[2]) > 8 * len(lens)
+    many = dtype == "bf16" and q.shape[0] * (q.shape[1] // k.shape[2]) > 8 * len(lens)
     p_step = P_STEP_TC if many else P_STEP[dtype]
     kn, vn = np.nan_to_num(f64(k), nan=0, posinf=0), np.nan_to_num(f64(v), nan=0, posinf=0)
     want, A, mag = R.attention(f64(q), start, lens, table, kn, vn, scale)
@@ -281,6 +281,8 @@ ATTN = [  # H, KV, hd, page, layout, lens, rows
     (4, 2, 128, 5, "slot", [333, 70], [33, 20]),  # many queries on pages that do not hold whole blocks
     (5, 1, 64, 7, "mixed", [100, 0, 31], [9, 4, 2]),
     (14, 2, 256, 16, "head", [500, 20], [9, 3]),
+    (4, 4, 208, 64, "slot", [1000, 65, 0, 130], [100, 20, 3, 128]),
+    (16, 1, 144, 32, "mixed", [90, 3000], [1, 9]),
 ]
 
 
