@@ -8,7 +8,7 @@
 //               past the sequence's end or on a bad page is read at a page
 //               coordinate outside the tensor, i.e. as zeros
 //   warps 1, 2  MMA issuers (one elected thread each): S_u = Q K_u^T (M = 128
-//               queries, N = 64 keys) into one of six score buffers in tensor
+//               queries, N = 64 keys) into one of five score buffers in tensor
 //               memory, and O += P_u V_u (P_u in tensor memory, V MN-major); one
 //               warp for both spent 0.9 us a sub-chunk on waits and issues
 //   warps 4-19  softmax, four sets of four warps: set u % 4 takes sub-chunk u, a
@@ -20,8 +20,8 @@
 // in the MMAs, and neither's latency is on the critical path.  (Two tiles of 128
 // queries taking turns on two buffers each, measured before: 1.3 us per 128
 // queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
-// TMEM: six score buffers of 64 columns, O of head_dim columns (head_dim above
-// 128: four buffers); P (bf16 pairs)
+// TMEM: five score buffers of 64 columns, Q, O of head_dim columns (head_dim
+// above 128: four buffers, Q in shared memory); P (bf16 pairs)
 // overwrites the second half of its scores, which are in registers by then.
 // P is rounded to bf16 once, as in the dense attention of a step: a second
 // product for the low part would cost half as much again on the tensor pipe.
@@ -45,13 +45,18 @@ constexpr int kThreads = 32 * kWarps;
 
 template <int DP>
 struct TcCfg {
-  static constexpr uint32_t kQ = 128u * DP * 2u;     // the Q tile: DP / 64 blocks of 128 rows x 128 bytes
+  // Q: in tensor memory (bf16 pairs), or, where that leaves too few score buffers, in shared memory: DP / 64 blocks of
+  // 128 rows x 128 bytes
+  static constexpr bool kQTmem = DP <= 128;
+  static constexpr uint32_t kQ = kQTmem ? 0u : 128u * DP * 2u;
   static constexpr uint32_t kTile = 64u * DP * 2u;   // K or V of a sub-chunk: DP / 64 blocks of 64 rows x 128 bytes
   // ring depths (sub-chunks) and score buffers: what shared memory (227 KB) and tensor memory (512 columns) hold
-  static constexpr uint32_t kKStages = DP == 256 ? 2 : 5, kVStages = DP == 256 ? 2 : 6, kBufs = DP == 256 ? 4 : 6;
+  static constexpr uint32_t kKStages = DP == 256 ? 2 : 6, kVStages = DP == 256 ? 2 : 7, kBufs = DP == 256 ? 4 : 5;
   static constexpr uint32_t kSmem = kQ + (kKStages + kVStages) * kTile + 1024u;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kO = 64 * kBufs;         // column of O
+  static constexpr uint32_t kQCol = 64 * kBufs;      // columns of Q and of O
+  static constexpr uint32_t kO = kQCol + (kQTmem ? 64 : 0);
+  static_assert(kO + DP <= kTmemCols, "tensor memory");
 };
 
 template <int ROWS>
@@ -209,7 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- MMA issuers: a warp runs as one, an elected lane issues
     const bool pv = warp == 2;
     const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
-    const uint64_t qd = sw128_desc(q_s), kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, kSub * 128u);
+    [[maybe_unused]] const uint64_t qd = sw128_desc(q_s);
+    const uint64_t kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, kSub * 128u);
     constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
     bool ok = true, any = false;
     uint32_t nseg = 0;                                        // segments
@@ -243,9 +249,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t kd = kd0 + st * kStep;
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk)
-              tc_mma(tmem + b * 64u, qd + (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3)),
-                     kd + (uint64_t)((kk >> 2) * (kSub * 128 >> 4) + 2 * (kk & 3)), id_s, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < DP / 16; ++kk) {
+              const uint64_t kdk = kd + (uint64_t)((kk >> 2) * (kSub * 128 >> 4) + 2 * (kk & 3));
+              if constexpr (C::kQTmem)
+                tc_mma_ts(tmem + b * 64u, tmem + C::kQCol + (uint32_t)(kk * 8), kdk, id_s, kk > 0 ? 1u : 0u);
+              else
+                tc_mma(tmem + b * 64u, qd + (uint64_t)((kk >> 2) * (16384 >> 4) + 2 * (kk & 3)), kdk, id_s,
+                       kk > 0 ? 1u : 0u);
+            }
             tc_commit(S_FULL(b));
             mbar_arrive(S_FULL(b));
             tc_commit(K_EMPTY(st));
@@ -297,17 +308,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = (int)(s1 - s0), ns = 2 * n;
       const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
       const Pairs pairs(sq, q0, G);
-      // queries -> shared memory (zero rows past nq, zero dims past head_dim); the last segment's MMAs have read theirs
-      // (O_FINAL)
-      for (int i = st_id; i < 128 * (DP / 8); i += 128 * (int)kSets) {
-        const int r = i / (DP / 8), c = i - r * (DP / 8);
-        const bool in = r < nq && c * 8 < hd;
-        load_query16(q_s + tile_off<128>(r, c),
-                     static_cast<const bf16 *>(a.q) + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0),
-                     in);
+      // queries (zero rows past nq, zero dims past head_dim) -> tensor memory, 32 dims of a row per thread, or shared
+      // memory; the last segment's MMAs have read theirs (O_FINAL)
+      const bf16 *qg = static_cast<const bf16 *>(a.q);
+      if constexpr (C::kQTmem) {
+        if (set < DP / 32) {
+          uint32_t qv[16];
+          const bf16 *src = qg + pairs.at(qi < nq ? qi : 0, seg.kvh, a.n_heads, hd);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int d = (int)set * 32 + c * 8;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (qi < nq && d < hd) v = *reinterpret_cast<const uint4 *>(src + d);
+            qv[4 * c] = v.x;
+            qv[4 * c + 1] = v.y;
+            qv[4 * c + 2] = v.z;
+            qv[4 * c + 3] = v.w;
+          }
+          tmem_st16u(tmem + C::kQCol + set * 16u + lane_off, qv);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+      } else {
+        for (int i = st_id; i < 128 * (DP / 8); i += 128 * (int)kSets) {
+          const int r = i / (DP / 8), c = i - r * (DP / 8);
+          const bool in = r < nq && c * 8 < hd;
+          load_query16(q_s + tile_off<128>(r, c), qg + pairs.at(in ? r : 0, seg.kvh, a.n_heads, hd) + (in ? c * 8 : 0), in);
+        }
+        load_query_wait();
+        fence_proxy_async_smem();
       }
-      load_query_wait();
-      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(Q_FULL);
       const bool used = q4 * 32 < nq;             // this warp has queries
@@ -408,9 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (left < kSub) {
           // Past the sequence's end its page holds anything: P is 0 there, V must be.  Boxes wholly past it came as
           // zeros; the rest of the last box is cleared after the copy and before P_FULL lets P V start.  (The stage held
-          // sub-chunk u - kVStages, whose P V was waited for by the issuer of this buffer's S, or here.)
+          // sub-chunk u - kVStages; the issuer of this buffer's S has waited for P V of sub-chunk u - kBufs.)
           const uint32_t st = u % kVStages, before = u - kVStages;
-          static_assert(kVStages <= kBufs, "the issuer of S_u has waited for P V of sub-chunk u - kBufs");
           if (kVStages < kBufs && u >= kVStages) {
             alive = __all_sync(0xffffffffu, wait_bounded(PV_DONE(before % kBufs), (before / kBufs) & 1u, abort_v, a.status));
             if (!alive) continue;
