@@ -6,8 +6,9 @@
 //   warps 0, 3  TMA producers of K and of V: the pages of a sub-chunk, boxes of
 //               `box` slots x 64 dims (128-byte swizzle), into a ring each; a box
 //               past the sequence's end or on a bad page is read at a page
-//               coordinate outside the tensor, i.e. as zeros
-//   warps 1, 2  MMA issuers (one elected thread each): S_u = Q K_u^T (M = 128
+//               coordinate outside the tensor, i.e. as zeros.  The warp looks 32
+//               boxes up at a time, one thread issues them
+//   warps 1, 2  MMA issuers (one thread each): S_u = Q K_u^T (M = 128
 //               queries, N = 64 keys) into one of five score buffers in tensor
 //               memory, and O += P_u V_u (P_u in tensor memory, V MN-major); one
 //               warp for both spent 0.9 us a sub-chunk on waits and issues
@@ -20,6 +21,15 @@
 // in the MMAs, and neither's latency is on the critical path.  (Two tiles of 128
 // queries taking turns on two buffers each, measured before: 1.3 us per 128
 // queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
+// What bounds a sub-chunk (4736 rows x 8192 keys x 4 heads, head dim 128, 72 us,
+// 1.10 PFLOP/s): the five score buffers.  From the issue of S to the end of P V
+// takes about 4300 cycles - 750 until S is seen, 600 for the maximum, 450 until
+// it is handed on, 1700 for the exponentials (of which four warps per scheduler
+// share the units), 750 for P V - and a fifth of that is the 870 cycles of a
+// sub-chunk, of which the products are 512.  Six buffers have no room beside Q in
+// tensor memory, and Q in shared memory makes S bound by its bytes there (384
+// cycles instead of 256); three sets that keep their 64 scores in registers took
+// 1.2 times as long, ring stages of two sub-chunks 1.04 times.
 // TMEM: five score buffers of 64 columns, Q, O of head_dim columns (head_dim
 // above 128: four buffers, Q in shared memory); P (bf16 pairs)
 // overwrites the second half of its scores, which are in registers by then.
@@ -111,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_max[kSets][128];   // [set] running maximum after the set's sub-chunk
   __shared__ float2 s_ml[kSets][128];   // [set] (maximum, sum) at the end of a segment
   __shared__ uint32_t s_bad[16];        // [sub-chunk % 16] its boxes on bad pages
+  __shared__ int2 s_box[2][32];         // [K, V][box of the producer's batch] slot, page
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sbase = (smem_u32(sm_raw) + 1023u) & ~1023u;
   uint8_t *sm = sm_raw + (sbase - smem_u32(sm_raw));
@@ -166,88 +177,107 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t stages = is_v ? kVStages : kKStages, ring = is_v ? v_s : k_s;
     const uint32_t full0 = is_v ? V_FULL(0) : K_FULL(0), empty0 = is_v ? V_EMPTY(0) : K_EMPTY(0);
     const CUtensorMap *map = is_v ? &vmap : &kmap;
-    const int nb = kSub / box;                    // boxes of a sub-chunk (of each 64-dim block)
-    const int my = lane % nb, blk = lane / nb;    // the lane's box: lanes 0 .. nb * DP / 64 - 1 issue
-    const bool mine = blk < DP / 64;
-    const uint32_t dst = (uint32_t)blk * (uint32_t)(kSub * 128) + (uint32_t)(my * box) * 128u;
-    // first key of the lane's box in sub-chunk h of the place, and its page (-1: none), looked up one ahead
-    auto key_of = [&](uint32_t h) { return seg.blk * kKC + (int)h * kSub + my * box; };
-    auto look = [&](uint32_t h) {
-      const int key = key_of(h);
-      return mine && key < seg.s.nk ? a.table[(size_t)seg.b * a.max_pages + div_page(a, (unsigned)key)] : -1;
-    };
-    int pg = look(0);
+    // A batch is 32 boxes: each lane looks its box up (one batch ahead) and leaves its place in shared memory, then one
+    // thread issues.  (Each sub-chunk looked up and issued by the whole warp, measured before: 1130 cycles a sub-chunk,
+    // more than anything else in the kernel took.)
+    const int nb = kSub / box, per = 32 / nb;  // boxes of a sub-chunk (of each 64-dim block), sub-chunks of a batch
+    int2 *const places = s_box[is_v];
     uint32_t st = 0, par = 1, u = 0;  // stage, its EMPTY parity, sub-chunk
     bool ok = true;
-    for (long long left = 2 * (rg.u1 - rg.u0); left > 0; --left, ++u) {
-      const int key = key_of(u & 1u), kvh = seg.kvh;
-      const bool in = mine && key < seg.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
-      const uint32_t bad = __ballot_sync(0xffffffffu, in && !good) & ((1u << nb) - 1u);  // lanes of block 0
-      const int w = good ? pg : a.pages.n_pages;  // outside the tensor: zeros
-      const int y = good ? key - (int)(div_page(a, (unsigned)key) * (unsigned)a.pages.page_size) : 0;
-      if (left > 1) {
-        if (u & 1u) advance<R, kKC>(a, seg, 1);
-        pg = look((u + 1) & 1u);
-      }
-      ok = __all_sync(0xffffffffu, wait_bounded(empty0 + 8u * st, par, abort_v, a.status));
-      if (!ok) break;
-      if (lane == 0) {
-        if (!is_v) {
-          s_bad[u & 15u] = bad;  // read by the softmax with the scores; sixteen sub-chunks later it has been
-          if (bad && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+    for (long long s0 = rg.u0; s0 < rg.u1 && ok;) {
+      const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
+      const int ns = 2 * (int)(s1 - s0), kvh = seg.kvh;
+      // first key of the lane's box in the batch of sub-chunk h of the segment, and its page (-1: none)
+      auto key_of = [&](int h) { return (unsigned)(seg.blk * kKC) + (unsigned)h * kSub + (unsigned)(lane * box); };
+      auto look = [&](int h) {
+        const unsigned key = key_of(h);
+        return h < ns && key < (unsigned)seg.s.nk ? a.table[(size_t)seg.b * a.max_pages + div_page(a, key)] : -1;
+      };
+      int pg = look(0);
+      for (int h0 = 0; h0 < ns && ok; h0 += per) {
+        const unsigned key = key_of(h0);
+        const bool in = key < (unsigned)seg.s.nk, good = in && pg >= 0 && pg < a.pages.n_pages;
+        const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+        // outside the tensor: zeros
+        places[lane] = make_int2(good ? (int)(key - div_page(a, key) * (unsigned)a.pages.page_size) : 0,
+                                 good ? pg : a.pages.n_pages);
+        __syncwarp();
+        pg = look(h0 + per);
+        const int n = min(per, ns - h0);
+        int done = 0;  // sub-chunks issued
+        if (elect_one()) {
+          for (; done < n; ++done) {
+            if (!wait_bounded(empty0 + 8u * st, par, abort_v, a.status)) break;
+            if (!is_v) {
+              const uint32_t mine = (bad >> (done * nb)) & ((1u << nb) - 1u);
+              s_bad[(u + (uint32_t)done) & 15u] = mine;  // read by the softmax with the scores, long before it is reused
+              if (mine && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+            }
+            const uint32_t bar = full0 + 8u * st, to = ring + st * C::kTile;
+            mbar_expect_tx(bar, C::kTile);
+            for (int x = 0; x < nb; ++x) {
+              const int2 at = places[done * nb + x];
+#pragma unroll
+              for (int blk = 0; blk < DP / 64; ++blk)
+                tma_box(to + (uint32_t)(blk * kSub * 128) + (uint32_t)(x * box) * 128u, map, blk * 64,
+                        head_first ? kvh : at.x, head_first ? at.x : kvh, at.y, bar);
+            }
+            if (++st == stages) {
+              st = 0;
+              par ^= 1u;
+            }
+          }
         }
-        mbar_expect_tx(full0 + 8u * st, C::kTile);
+        // the issuing thread need not be the same one each time
+        done = (int)__reduce_max_sync(0xffffffffu, (unsigned)done);
+        ok = done == n;
+        u += (uint32_t)done;
+        st = u % stages;
+        par = ((u / stages) & 1u) ^ 1u;
+        __syncwarp();
       }
-      __syncwarp();
-      if (mine)
-        tma_box(ring + st * C::kTile + dst, map, blk * 64, head_first ? kvh : y, head_first ? y : kvh, w,
-                full0 + 8u * st);
-      if (++st == stages) {
-        st = 0;
-        par ^= 1u;
-      }
+      advance<R, kKC>(a, seg, ns / 2);
+      s0 = s1;
     }
     if (!ok)  // wait, bounded, for the copies still in flight: the last phase of every stage
       for (uint32_t s = 0; s < stages; ++s)
         if (u > s) wait_drain(full0 + 8u * s, ((u - 1 - s) / stages) & 1u);
   } else if (warp <= 2) {
-    // ---- MMA issuers: a warp runs as one, an elected lane issues
-    const bool pv = warp == 2;
-    const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
-    [[maybe_unused]] const uint64_t qd = sw128_desc(q_s);
-    const uint64_t kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, kSub * 128u);
-    constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
-    bool ok = true, any = false;
-    uint32_t nseg = 0;                                        // segments
-    uint32_t st = 0, st_par = 0, b = 0, b_par = 0;            // stage and buffer of the sub-chunk, their FULL parities
-    const uint32_t stages = pv ? kVStages : kKStages;
-    bool fresh = true;                                        // the buffers have not been used yet
-    auto step = [&]() {
-      if (++st == stages) {
-        st = 0;
-        st_par ^= 1u;
-      }
-      if (++b == kBufs) {
-        b = 0;
-        b_par ^= 1u;
-        fresh = false;
-      }
-    };
-    auto wait = [&](uint32_t bar, uint32_t par) {
-      ok = ok && __all_sync(0xffffffffu, wait_bounded(bar, par & 1u, abort_v, a.status));
-      return ok;
-    };
-    for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
-      const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-      const int ns = 2 * (int)(s1 - s0);
-      if (!pv) {
-        if (!wait(Q_FULL, nseg)) break;
-        for (int i = 0; i < ns; ++i, step()) {
-          // the buffer's last P V has read its P
-          if (!wait(K_FULL(st), st_par) || (!fresh && !wait(PV_DONE(b), b_par ^ 1u))) break;
-          tc_fence_after();
-          const uint64_t kd = kd0 + st * kStep;
-          if (elect_one()) {
+    // ---- MMA issuers: one thread waits and issues
+    if (elect_one()) {
+      const bool pv = warp == 2;
+      const uint32_t id_s = idesc_bf16(128, kSub), id_o = idesc_bf16_bmn(128, DP);
+      [[maybe_unused]] const uint64_t qd = sw128_desc(q_s);
+      const uint64_t kd0 = sw128_desc(k_s), vd0 = sw128_mn_desc(v_s, kSub * 128u);
+      constexpr uint64_t kStep = C::kTile >> 4;  // descriptor distance of two stages
+      bool ok = true, any = false;
+      uint32_t nseg = 0;                                        // segments
+      uint32_t st = 0, st_par = 0, b = 0, b_par = 0;            // stage and buffer of the sub-chunk, their FULL parities
+      const uint32_t stages = pv ? kVStages : kKStages;
+      auto step = [&]() {
+        if (++st == stages) {
+          st = 0;
+          st_par ^= 1u;
+        }
+        if (++b == kBufs) {
+          b = 0;
+          b_par ^= 1u;
+        }
+      };
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        ok = wait_bounded(bar, par & 1u, abort_v, a.status);
+        return ok;
+      };
+      for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
+        const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
+        const int ns = 2 * (int)(s1 - s0);
+        if (!pv) {
+          if (!wait(Q_FULL, nseg)) break;
+          for (int i = 0; i < ns; ++i, step()) {
+            // the buffer's last P V has read its P (the first time there is none, and that parity has passed)
+            if (!wait(K_FULL(st), st_par) || !wait(PV_DONE(b), b_par ^ 1u)) break;
+            tc_fence_after();
+            const uint64_t kd = kd0 + st * kStep;
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
               const uint64_t kdk = kd + (uint64_t)((kk >> 2) * (kSub * 128 >> 4) + 2 * (kk & 3));
@@ -260,16 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(S_FULL(b));
             mbar_arrive(S_FULL(b));
             tc_commit(K_EMPTY(st));
+            any = true;
           }
-          __syncwarp();
-          any = true;
-        }
-      } else {
-        for (int i = 0; i < ns; ++i, step()) {
-          if (!wait(V_FULL(st), st_par) || !wait(P_FULL(b), b_par)) break;
-          tc_fence_after();
-          const uint64_t vd = vd0 + st * kStep;
-          if (elect_one()) {
+        } else {
+          for (int i = 0; i < ns; ++i, step()) {
+            if (!wait(V_FULL(st), st_par) || !wait(P_FULL(b), b_par)) break;
+            tc_fence_after();
+            const uint64_t vd = vd0 + st * kStep;
 #pragma unroll
             for (int kk = 0; kk < kSub / 16; ++kk)
               tc_mma_ts(tmem + C::kO, tmem + b * 64u + 32u + (uint32_t)(kk * 8), vd + (uint64_t)(kk * (2048 >> 4)), id_o,
@@ -277,20 +304,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(PV_DONE(b));
             tc_commit(V_EMPTY(st));
             if (i == ns - 1) tc_commit(O_FINAL);
+            any = true;
           }
-          __syncwarp();
-          any = true;
         }
+        if (!ok) break;
+        advance<R, kKC>(a, seg, ns / 2);
+        s0 = s1;
       }
-      if (!ok) break;
-      advance<R, kKC>(a, seg, ns / 2);
-      s0 = s1;
-    }
-    if (!ok && any) {
-      const uint32_t drain = DRAIN + (pv ? 8u : 0u);
-      if (elect_one()) tc_commit(drain);
-      __syncwarp();
-      wait_drain(drain, 0);
+      if (!ok && any) {
+        const uint32_t drain = DRAIN + (pv ? 8u : 0u);
+        tc_commit(drain);
+        wait_drain(drain, 0);
+      }
     }
   } else if (warp >= kSoft0) {
     // ---- softmax
