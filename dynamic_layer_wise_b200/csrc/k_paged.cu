@@ -279,7 +279,6 @@ cudaError_t launch_page_table(const int32_t *lens, int B, int page_size, int max
   int per = (B + 148 * 4 - 1) / (148 * 4);
   if (per > kTabThreads) per = kTabThreads;
   const dim3 grid((B + per - 1) / per, (max_pages + kTabCols - 1) / kTabCols);
-  if (grid.y > 65535) return cudaErrorInvalidValue;
   return launch_pdl(k_page_table, grid, dim3(kTabThreads), 0, s, lens, B, page_size, max_pages, n_pages, pool, n_pool,
                     first, per, table, held, next, status);
 }
@@ -299,7 +298,6 @@ cudaError_t launch_paged_write(const float *qkv, int max_rows, const int32_t *n_
   // a row's items in as few slices as fit a CTA, in equal parts
   const int items = (n_heads + 2 * pages.n_kv_heads) * (pages.head_dim / 16);
   const int slices = (items + kWriteMax - 1) / kWriteMax;
-  if (slices > 65535) return cudaErrorInvalidValue;
   const int threads = ((items + slices - 1) / slices + 31) / 32 * 32;
   const dim3 grid(max_rows, slices);
   if (pages.dtype == DCU_BF16)

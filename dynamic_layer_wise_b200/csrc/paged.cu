@@ -30,6 +30,11 @@ int pg_cuda(cudaError_t e, const char *call) noexcept {
   return DCU_ECUDA;
 }
 
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 bool mis(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 const char *bad_pages(const dcu_pages *p) {
@@ -55,7 +60,7 @@ int dcu_page_table(const int32_t *lens, int32_t B, int32_t page_size, int32_t ma
                    const int32_t *pool, int32_t n_pool, const int32_t *first, int32_t *table, int32_t *held,
                    int32_t *next, int32_t *status, dcu_stream_t stream) {
   if (!lens || !table || !held || !next || B <= 0 || B > kPagedMaxB || page_size <= 0 || max_pages <= 0 ||
-      n_pages <= 0 || n_pool < 0 || (int64_t)n_pages * page_size >= (1ll << 31) || next == first)
+      max_pages > (1 << 27) || n_pages <= 0 || n_pool < 0 || (int64_t)n_pages * page_size >= (1ll << 31) || next == first)
     return pg_fail(DCU_EINVAL, "dcu_page_table: bad argument");
   if (!pool && n_pool != n_pages && n_pool != 0)
     return pg_fail(DCU_EINVAL, "dcu_page_table: without a pool, n_pool must be n_pages");
@@ -99,6 +104,10 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
       (pages->n_kv_heads > 1 && !pages->head_stride))
     return pg_fail(DCU_EINVAL, "dcu_paged_write: pages with a zero stride cannot be written");
   if (max_rows == 0) return DCU_OK;
+  if (pages->k == pages->v) return pg_fail(DCU_EINVAL, "dcu_paged_write: K and V share their pages");
+  const int64_t es = pages->dtype == DCU_BF16 ? 2 : 4, rh = (int64_t)max_rows * pages->head_dim;
+  if (overlap(q, rh * n_heads * es, qkv, rh * (n_heads + 2ll * pages->n_kv_heads) * 4))
+    return pg_fail(DCU_EINVAL, "dcu_paged_write: q overlaps qkv");
   return pg_cuda(launch_paged_write(qkv, max_rows, n_rows, row_pos, slot, reinterpret_cast<const float2 *>(rope),
                                     max_pos, n_heads, *pages, q, status, (cudaStream_t)stream),
                  "dcu_paged_write");
@@ -121,8 +130,11 @@ int dcu_paged_attention(const void *q, int32_t max_rows, const int32_t *row_star
     return pg_fail(DCU_EINVAL, "dcu_paged_attention: bad argument");
   if (mis(q, 16) || mis(out, 16) || mis(workspace, 16))
     return pg_fail(DCU_EINVAL, "dcu_paged_attention: q, out and workspace must be 16-byte aligned");
-  if (max_rows > 0 && q == out) return pg_fail(DCU_EINVAL, "dcu_paged_attention: out may not be q");
   if (max_rows == 0) return DCU_OK;
+  if ((int64_t)max_rows * (n_heads / pages->n_kv_heads) >= (1ll << 30))  // queries of a kv head are counted in 32 bits
+    return pg_fail(DCU_EINVAL, "dcu_paged_attention: too many rows x heads of a group");
+  const int64_t qb = (int64_t)max_rows * n_heads * pages->head_dim * (pages->dtype == DCU_BF16 ? 2 : 4);
+  if (overlap(q, qb, out, qb)) return pg_fail(DCU_EINVAL, "dcu_paged_attention: out may not overlap q");
   if (!workspace || workspace_bytes < paged_attention_workspace(*pages))
     return pg_fail(DCU_EINVAL, "dcu_paged_attention: workspace smaller than dcu_paged_attention_workspace");
   PagedAttnArgs a;

@@ -378,8 +378,8 @@ typedef struct {
  * pool entry outside [0, n_pages) becomes -1 (DCU_ST_BAD_PAGE).
  * table: dev int32 [B][max_pages], every entry written; held: dev int32 [B], the
  * pages each request got; next: dev int32, *first + the pages given out -- the
- * `first` of the next call on the same pool.  B <= 65536.  `next` may not alias
- * `first`. */
+ * `first` of the next call on the same pool.  B <= 65536, max_pages <= 2^27.
+ * `next` may not alias `first`. */
 int dcu_page_table(const int32_t *lens, int32_t B, int32_t page_size, int32_t max_pages, int32_t n_pages,
                    const int32_t *pool, int32_t n_pool, const int32_t *first, int32_t *table, int32_t *held,
                    int32_t *next, int32_t *status, dcu_stream_t stream);
@@ -412,8 +412,8 @@ int dcu_rope_table(float *tab, int32_t max_pos, int32_t head_dim, float theta, d
  * outside [0, n_pages * page_size) is not written (a slot of -1 silently).  A
  * row_pos outside [0, max_pos) gives a zero query and no K/V write
  * (DCU_ST_BAD_ROW; not looked at without rope).  Strides must be positive where
- * their dimension is above 1, and no two slots may overlap.  Two rows with the same slot
- * leave a mixture of both there. */
+ * their dimension is above 1, no two slots may overlap, K and V are two arrays, and
+ * q may not overlap qkv.  Two rows with the same slot leave a mixture of both there. */
 int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, const int32_t *row_pos,
                     const int32_t *slot, const float *rope, int32_t max_pos, int32_t n_heads,
                     const dcu_pages *pages, void *q, int32_t *status, dcu_stream_t stream);
@@ -429,7 +429,8 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
  * The keys are split over the SMs and joined in a fixed order: equal inputs
  * give equal bits.  workspace: dev, 16-byte aligned, at least
  * dcu_paged_attention_workspace bytes, any content; calls that may overlap (on
- * other streams, or in graphs replayed together) need one each.  B <= 65536. */
+ * other streams, or in graphs replayed together) need one each.  B <= 65536,
+ * max_rows * (n_heads / n_kv_heads) < 2^30. */
 int dcu_paged_attention(const void *q, int32_t max_rows, const int32_t *row_start, int32_t B, const int32_t *kv_len,
                         const int32_t *table, int32_t max_pages, int32_t n_heads, const dcu_pages *pages, float scale,
                         void *out, void *workspace, int64_t workspace_bytes, int32_t *status, dcu_stream_t stream);

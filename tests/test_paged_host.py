@@ -110,3 +110,19 @@ def test_binding_refuses_cpu_tensors_and_wrong_types(L):
         dcu.dcu_paged_write(torch.zeros(3, 1024), i, i, i, None, k, k, 8)
     with pytest.raises(ValueError):
         dcu.dcu_rope_table(0, 64, device="cuda:0")
+
+
+def test_sizes_and_overlaps_that_are_refused(L):
+    # a launch's second grid dimension ends at 65535: 4096 table columns per block
+    assert _call(L.dcu_page_table, TABLE, max_pages=(1 << 27) + 1) == dcu.DCU_EINVAL
+    # queries of a kv head, 2^27 rows x 8 heads
+    assert _call(L.dcu_paged_attention, ATTN, max_rows=1 << 27, n_heads=32, out=1 << 46) == dcu.DCU_EINVAL
+    # 4 rows x 8 heads x 64 dims x 2 bytes of q end where out may begin
+    assert _call(L.dcu_paged_attention, ATTN, out=P + 4096 - 16) == dcu.DCU_EINVAL
+    assert _call(L.dcu_paged_attention, ATTN, q=2 * P, out=P + 16) == dcu.DCU_EINVAL
+    # q may not be written over the float32 rows that are still to be read, nor K over V
+    other = dict(pages=dict(v=1 << 30), q=P + 4 * 16 * 64 * 4 - 16)
+    assert _call(L.dcu_paged_write, WRITE, **other) == dcu.DCU_EINVAL
+    assert b"overlaps" in L.dcu_last_error(None)
+    assert _call(L.dcu_paged_write, WRITE, q=1 << 30) == dcu.DCU_EINVAL
+    assert b"share" in L.dcu_last_error(None)
