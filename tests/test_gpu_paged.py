@@ -346,6 +346,43 @@ def test_paged_attention_bad_pages_and_lengths(dtype):
         assert st.item() == R.BAD_PAGE and torch.equal(out[:7], ref[:7])
 
 
+@pytest.mark.parametrize("page,rows", [(16, [130, 9]), (32, [40, 33]), (64, [200, 1]), (16, [1, 1]), (5, [3, 40])])
+def test_paged_attention_bad_pages_all_along(page, rows):
+    """A fifth of the pages of long sequences is not there."""
+    q, start, lens, table, k, v = case_inputs(60 + page, "bf16", 4, 2, 128, page, "head", [3001, 700], rows)
+    rng = np.random.default_rng(page)
+    bad = np.where((rng.random(table.shape) < 0.2) & (table >= 0), np.where(rng.random(table.shape) < 0.5, -1, 10 ** 9),
+                   table).astype(np.int32)
+    st = status_word()
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(bad), k, v, status=st)
+    assert st.item() == R.BAD_PAGE
+    check_attention(out, q, start, lens, bad, k, v, "bf16", 128 ** -0.5)
+
+
+@pytest.mark.parametrize("H,KV,hd,page,rows,n", [(4, 2, 64, 16, 20, 90), (8, 1, 128, 64, 17, 60), (2, 2, 256, 32, 30, 40)])
+def test_paged_attention_many_items_in_a_range(H, KV, hd, page, rows, n):
+    rng = np.random.default_rng(n)
+    q, start, lens, table, k, v = case_inputs(70 + n, "bf16", H, KV, hd, page, "slot", list(rng.integers(0, 500, n)),
+                                              list(rng.integers(0, 2 * rows, n)))
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v)
+    check_attention(out, q, start, lens, table, k, v, "bf16", hd ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 90), ("f32", 9)])
+@pytest.mark.parametrize("n", [40, 5000])
+def test_paged_attention_keeps_a_bad_query_to_itself(dtype, rows, n):
+    """NaN in a query makes its own output NaN, whether its keys are split or not, and no other."""
+    q, start, lens, table, k, v = case_inputs(8, dtype, 4, 2, 64, 16, "slot", [n], [rows])
+    call = lambda x: dcu.dcu_paged_attention(x, i32(start), i32(lens), i32(table), k, v)[:rows]
+    ref = call(q)
+    x = q.clone()
+    x[rows // 2, 1, 5] = float("nan")
+    out = call(x)
+    hit = torch.zeros(rows, 4, 64, dtype=torch.bool, device="cuda")
+    hit[rows // 2, 1] = True
+    assert out[hit].isnan().all() and torch.equal(out[~hit], ref[~hit])
+
+
 def test_paged_attention_row_starts_outside_the_rows():
     q, start, lens, table, k, v = case_inputs(7, "bf16", 4, 2, 64, 16, "slot", [50, 60], [2, 3], tail=0)
     out = torch.full_like(q, 3.0)
