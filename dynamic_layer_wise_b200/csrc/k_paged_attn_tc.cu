@@ -48,6 +48,9 @@ namespace {
 
 constexpr int kKC = 128;              // keys of a unit
 constexpr int kSub = 64;              // keys of a sub-chunk
+// Units that a change of items costs (O out, Q in, the pipeline refilled: 5 us, a unit takes 1 us).  Measured with 4, 8
+// and 12: 60 heads x 100 rows x 8192 keys 63, 56 and 56 us, 50 heads of 64 dims 39, 39 and 43.
+constexpr int kTurn = 8;
 constexpr uint32_t kSets = 4;         // softmax sets
 constexpr int kSoft0 = 4;             // first softmax warp
 constexpr int kWarps = kSoft0 + 4 * kSets;
@@ -118,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int abort_flag;
   __shared__ long long s_scan[2 * kWarps];
   __shared__ Place s_place;
+  __shared__ Range s_range;
   __shared__ float s_max[kSets][128];   // [set] running maximum after the set's sub-chunk
   __shared__ float2 s_ml[kSets][128];   // [set] (maximum, sum) at the end of a segment
   __shared__ uint32_t s_bad[16];        // [sub-chunk % 16] its boxes on bad pages
@@ -162,14 +166,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_enter();
   fence_proxy_async_global();  // the pages may have been written by the kernel just waited for
   tc_fence_before();
-  Place seg;
-  const Range rg = find_range<R, kKC, kWarps>(a, seg, &s_place, s_scan, 1);  // (a barrier inside)
+  find_range<R, kKC, kWarps>(a, &s_place, &s_range, s_scan, 1, kTurn);  // (a barrier inside)
+  Place seg = s_place;
+  const int units = s_range.any ? (int)(s_range.u1 - s_range.u0) : 0;
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   volatile int *abort_v = &abort_flag;
   const int KV = a.pages.n_kv_heads, G = a.n_heads / KV, hd = a.pages.head_dim;
 
-  if (!rg.any) {
+  if (!units) {
     if (tid == 0) shares[blockIdx.x].last = -1;
   } else if (warp == 0 || warp == 3) {
     // ---- TMA producers
@@ -184,9 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int2 *const places = s_box[is_v];
     uint32_t st = 0, par = 1, u = 0;  // stage, its EMPTY parity, sub-chunk
     bool ok = true;
-    for (long long s0 = rg.u0; s0 < rg.u1 && ok;) {
-      const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-      const int ns = 2 * (int)(s1 - s0), kvh = seg.kvh;
+    for (int left = units; left > 0 && ok;) {
+      const int ns = 2 * min(left, seg.s.nblk - seg.blk), kvh = seg.kvh;
       // first key of the lane's box in the batch of sub-chunk h of the segment, and its page (-1: none)
       auto key_of = [&](int h) { return (unsigned)(seg.blk * kKC) + (unsigned)h * kSub + (unsigned)(lane * box); };
       auto look = [&](int h) {
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       advance<R, kKC>(a, seg, ns / 2);
-      s0 = s1;
+      left -= ns / 2;
     }
     if (!ok)  // wait, bounded, for the copies still in flight: the last phase of every stage
       for (uint32_t s = 0; s < stages; ++s)
@@ -268,9 +272,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_bounded(bar, par & 1u, abort_v, a.status);
         return ok;
       };
-      for (long long s0 = rg.u0; s0 < rg.u1 && ok; ++nseg) {
-        const long long s1 = min(rg.u1, s0 + (seg.s.nblk - seg.blk));
-        const int ns = 2 * (int)(s1 - s0);
+      for (int left = units; left > 0 && ok; ++nseg) {
+        const int ns = 2 * min(left, seg.s.nblk - seg.blk);
         if (!pv) {
           if (!wait(Q_FULL, nseg)) break;
           for (int i = 0; i < ns; ++i, step()) {
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         advance<R, kKC>(a, seg, ns / 2);
-        s0 = s1;
+        left -= ns / 2;
       }
       if (!ok && any) {
         const uint32_t drain = DRAIN + (pv ? 8u : 0u);
@@ -327,10 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sc = a.scale_log2;
     uint32_t g = 0, nseg = 0;  // chunks of the CTA before the segment, segments
     bool alive = true;
-    for (long long s0 = rg.u0; s0 < rg.u1; ++nseg) {
+    for (int at = 0; at < units; ++nseg) {
       const Seq &sq = seg.s;
-      const long long s1 = min(rg.u1, s0 + (sq.nblk - seg.blk));
-      const int n = (int)(s1 - s0), ns = 2 * n;
+      const int n = min(units - at, sq.nblk - seg.blk), ns = 2 * n;
       const int q0 = seg.tile * sq.tq, nq = min(sq.tq, sq.nq - q0);
       const Pairs pairs(sq, q0, G);
       // queries (zero rows past nq, zero dims past head_dim) -> tensor memory, 32 dims of a row per thread, or shared
@@ -487,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_ml[set][qi] = make_float2(m_own, l_run);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + q4) : "memory");
       const bool starts = seg.blk == 0, ends = n == sq.nblk - seg.blk;
-      const int slot = s0 == rg.u0 ? 0 : 1;
+      const int slot = at ? 1 : 0;
       if (alive && used) {
         tc_fence_after();
         float m = -INFINITY, l = 0.f;
@@ -526,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (set == 0 && qi < nq && !(starts && ends)) part_ml[share * R + qi] = make_float2(m, l);
         tc_fence_before();
       }
-      if (s1 == rg.u1 && st_id == 0) {
+      if (at + n == units && st_id == 0) {
         Share sh;
-        sh.last = starts && !ends && alive ? rg.of(s0 + sq.nblk - 1) : -1;
+        sh.last = starts && !ends && alive ? s_range.of(s_range.u0 + at + sq.nblk - 1) : -1;
         sh.row0 = sq.row0;
         sh.q0 = q0;
         sh.nq = nq;
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += (uint32_t)n;
       advance<R, kKC>(a, seg, n);
-      s0 = s1;
+      at += n;
     }
   }
   __syncthreads();

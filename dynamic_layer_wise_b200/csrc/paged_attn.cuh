@@ -79,19 +79,16 @@ __device__ __forceinline__ void advance(const PagedAttnArgs &a, Place &p, int n)
 
 
 // The range [u0, u1) of a CTA.  Either the line is cut evenly (range i of the
-// launch holds q + 1 units when i < rem, else q), or, for one sequence whose
-// items are few, every item of q units is cut into `parts` ranges: then no CTA
-// works on two items, and an item has fewer shares.
+// launch holds q + 1 units when i < rem, else q), or, where the items are few,
+// every item is cut by itself into equal parts: then no CTA works on two items,
+// and an item has fewer shares.
 struct Range {
   long long u0, u1, q;
-  int rem, parts;  // parts 0: the even cut
+  int rem, last;  // last -1: the even cut; else the last range of the only item, whose units count from 0
   bool any;
-  // the range that holds unit u
+  // the range that holds unit u, the last one of an item that the range has a part of
   __device__ __forceinline__ int of(long long u) const {
-    if (parts) {
-      const long long item = u / q;
-      return (int)(item * parts + ((u - item * q + 1) * parts - 1) / q);
-    }
+    if (last >= 0) return last;
     const long long wide = rem * (q + 1);
     return u < wide ? (int)(u / (q + 1)) : rem + (int)((u - wide) / q);
   }
@@ -105,7 +102,7 @@ __device__ __forceinline__ long long div_ll(long long a, int b) {
 // one sequence (B == 1) needs neither the scan nor a barrier.
 __device__ __forceinline__ void cut_even(Range &rg, long long total, int ranges) {
   const int bid = (int)blockIdx.x;
-  rg.parts = 0;
+  rg.last = -1;
   rg.any = bid < ranges;
   rg.q = ranges ? div_ll(total, ranges) : 0;
   rg.rem = (int)(total - rg.q * ranges);
@@ -120,13 +117,26 @@ __device__ __forceinline__ void locate(Place &p, long long off) {
   p.tile = (int)(item - (long long)p.kvh * p.s.tiles);
 }
 
-// All W warps of the CTA: its range, and its first place in `first`.  A launch
-// uses the whole grid unless that leaves a range less than `least` units of an
-// item that is cut: as many ranges as there are items, or as many as have
-// `least` units, whichever is more.
+// part `part` of `parts` of item `item` of sequence p.s
+__device__ __forceinline__ void cut_item(Range &rg, Place &p, int item, int part, int parts, int first_range) {
+  rg.u0 = div_ll((long long)part * p.s.nblk, parts);
+  rg.u1 = div_ll((long long)(part + 1) * p.s.nblk, parts);
+  rg.last = first_range + parts - 1;
+  p.blk = (int)rg.u0;
+  p.kvh = item / p.s.tiles;
+  p.tile = item - p.kvh * p.s.tiles;
+}
+
+// All W warps of the CTA: its range and its first place, in shared memory (each
+// thread's own copies of what the search holds would cost the kernels registers).
+// A launch uses the whole grid unless that leaves a range less than `least` units
+// of an item that is cut: as many ranges as there are items, or as many as have
+// `least` units, whichever is more.  The cut is by items where that makes the
+// longest range at most `turn` units longer than the even cut does: what a
+// CTA's change of items costs.
 template <int R, int KB, int W>
-__device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first, Place *place, long long *scan,
-                                            int least) {
+__device__ __forceinline__ void find_range(const PagedAttnArgs &a, Place *place, Range *range, long long *scan,
+                                           int least, int turn) {
   const int KV = a.pages.n_kv_heads;
   Range rg;
   if (a.B == 1) {
@@ -138,21 +148,20 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
     const int ranges = (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least)));
     cut_even(rg, total, ranges);
     if (total > 0 && items <= ranges) {
-      // cut item by item when that adds no more to the longest range than `least` units, which a second item would cost
       const int f = ranges / (int)items;
-      if ((p.s.nblk + f - 1) / f <= (int)rg.q + (rg.rem ? 1 : 0) + least) {
-        const int item = (int)blockIdx.x / f, part = (int)blockIdx.x - item * f;
-        rg.parts = f;
+      if ((p.s.nblk + f - 1) / f <= (int)rg.q + (rg.rem ? 1 : 0) + turn) {
+        const int item = (int)blockIdx.x / f;
         rg.any = item < items;
-        rg.q = p.s.nblk;
-        rg.u0 = (long long)item * p.s.nblk + div_ll((long long)part * p.s.nblk, f);
-        rg.u1 = (long long)item * p.s.nblk + div_ll((long long)(part + 1) * p.s.nblk, f);
+        if (rg.any) cut_item(rg, p, item, (int)blockIdx.x - item * f, f, item * f);
       }
     }
-    if (rg.any) locate(p, rg.u0);
-    first = p;
-    __syncthreads();  // (the callers' shared state is set up by one thread)
-    return rg;
+    if (rg.any && rg.last < 0) locate(p, rg.u0);
+    if (threadIdx.x == 0) {
+      *place = p;
+      *range = rg;
+    }
+    __syncthreads();
+    return;
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + 32 * W - 1) / (32 * W);
@@ -186,7 +195,64 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
     total += scan[i];
     items += scan[W + i];
   }
-  cut_even(rg, total, (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least))));
+  const int ranges = (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least)));
+  if (items > 0 && items <= (int)gridDim.x) {
+    // parts of at most cut[c] units: the first c that gives no more parts than there are CTAs.  The counts (at most
+    // items + total / cut, below 300) are added up packed, 16 bits for each c.
+    constexpr int NC = 4;
+    __shared__ unsigned long long s_cnt[W];
+    const int even = (int)div_ll(total + ranges - 1, ranges);
+    const int cut[NC] = {even, even + turn / 4, even + turn / 2, even + turn};
+    unsigned long long n = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = per == 1 ? p.s : seq_of<R, KB>(a, b);
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        n += (unsigned long long)(KV * s.tiles * (((unsigned)s.nblk + cut[c] - 1u) / (unsigned)cut[c])) << (16 * c);
+    }
+    unsigned long long upto = n, before = 0, all4 = 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) s_cnt[warp] = upto;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i == warp) before = all4;
+      all4 += s_cnt[i];
+    }
+    before += upto - n;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int all = (int)(all4 >> (16 * c) & 0xffffu), mine_r = (int)(n >> (16 * c) & 0xffffu);
+      if (all > (int)gridDim.x) continue;
+      int at_r = (int)(before >> (16 * c) & 0xffffu);
+      const int bid = (int)blockIdx.x;
+      if (bid >= at_r && bid < at_r + mine_r) {  // exactly one thread, or none
+        int f = 0;
+        for (p.b = b0; p.b < b1; ++p.b) {
+          if (per > 1) p.s = seq_of<R, KB>(a, p.b);
+          f = (p.s.nblk + cut[c] - 1) / cut[c];
+          if (bid < at_r + KV * p.s.tiles * f) break;
+          at_r += KV * p.s.tiles * f;
+        }
+        const int item = (bid - at_r) / f;
+        cut_item(rg, p, item, bid - at_r - item * f, f, at_r + item * f);
+        rg.any = true;
+        *place = p;
+        *range = rg;
+      }
+      if (tid == 0 && bid >= all) {
+        rg.any = false;
+        *range = rg;
+      }
+      __syncthreads();
+      return;
+    }
+  }
+  cut_even(rg, total, ranges);
   long long at = base + x - mine;
   if (rg.any && rg.u0 >= at && rg.u0 < at + mine) {  // exactly one thread
     if (per > 1)
@@ -198,9 +264,8 @@ __device__ __forceinline__ Range find_range(const PagedAttnArgs &a, Place &first
     locate(p, rg.u0 - at);
     *place = p;
   }
+  if (tid == 0) *range = rg;
   __syncthreads();
-  first = *place;
-  return rg;
 }
 
 // The (row, head) pairs of a tile: query r is row r0 + (h0 + r) / G, head h0 + r
