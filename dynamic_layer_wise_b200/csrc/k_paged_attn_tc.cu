@@ -1,7 +1,7 @@
 // Paged attention of many query rows per sequence on the 5th-gen tensor cores
-// (bf16).  Same line of work, shares and merge as
-// k_paged_attn.cu, with items of up to 128 queries (one TMEM lane each) and
-// units of 128 keys, worked in sub-chunks of 64:
+// (bf16).  Same line of work, shares and merge as k_paged_attn.cu, with items of
+// up to 128 queries (one TMEM lane each) and units of 128 keys, worked in
+// sub-chunks of 64:
 //
 //   warps 0, 3  TMA producers of K and of V: the pages of a sub-chunk, boxes of
 //               `box` slots x 64 dims (128-byte swizzle), into a ring each; a box
@@ -21,19 +21,24 @@
 // in the MMAs, and neither's latency is on the critical path.  (Two tiles of 128
 // queries taking turns on two buffers each, measured before: 1.3 us per 128
 // queries x 128 keys, bound by the chain softmax - P V - S of each tile.)
-// What bounds a sub-chunk (4736 rows x 8192 keys x 4 heads, head dim 128, 72 us,
-// 1.10 PFLOP/s): the five score buffers.  From the issue of S to the end of P V
-// takes about 4300 cycles - 750 until S is seen, 600 for the maximum, 450 until
-// it is handed on, 1700 for the exponentials (of which four warps per scheduler
-// share the units), 750 for P V - and a fifth of that is the 870 cycles of a
-// sub-chunk, of which the products are 512.  Six buffers have no room beside Q in
+//
+// What bounds a sub-chunk (4736 rows x 8192 keys x 4 heads, head dim 128: 72 to 78
+// us with the GPU's clock, 1.02 to 1.10 PFLOP/s): the five score buffers.  From
+// the issue of S to the end of P V takes about 4300 cycles - 750 until S is seen,
+// 600 for the maximum, 450 until it is handed on, 1700 for the exponentials (whose
+// units four warps of a scheduler share), 750 for P V - and a fifth of that is the
+// 870 cycles of a sub-chunk, of which the products are 512.  Six buffers have no room beside Q in
 // tensor memory, and Q in shared memory makes S bound by its bytes there (384
 // cycles instead of 256); three sets that keep their 64 scores in registers took
-// 1.2 times as long, ring stages of two sub-chunks 1.04 times.
+// 1.2 times as long, ring stages of two sub-chunks 1.04 times, and the next item's
+// queries loaded under the last one's epilogue (for registers) 1.05 times.
+// Shorter calls are bound by what surrounds the loop: 161 rows x 8192 keys of 32
+// heads take 47 us, of which 32 are the loop (64 sub-chunks), 9.5 the way to the
+// first P V (search 1.6, Q 2, first keys 2.5, first softmax 3), 5 the merge.
+//
 // TMEM: five score buffers of 64 columns, Q, O of head_dim columns (head_dim
-// above 128: four buffers, Q in shared memory); P (bf16 pairs)
-// overwrites the second half of its scores, which are in registers by then.
-// P is rounded to bf16 once, as in the dense attention of a step: a second
+// above 128: four buffers, Q in shared memory); P (bf16 pairs) overwrites the
+// second half of its scores, which are in registers by then.  P is rounded to bf16 once, as in the dense attention of a step: a second
 // product for the low part would cost half as much again on the tensor pipe.
 //
 // Every mbarrier wait is bounded; on expiry the CTA sets DCU_ST_TIMEOUT, drains
