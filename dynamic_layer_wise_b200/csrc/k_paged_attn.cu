@@ -931,7 +931,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);
   PageMaps m = {};
-  if (a.scale_log2 > 0.f && a.pages.page_size % 16 == 0 && page_maps(a.pages, tc_box_keys(a.pages), &m))
+  if (a.scale_log2 > 0.f && a.pages.page_size % 8 == 0 && page_maps(a.pages, tc_box_keys(a.pages), &m))
     return launch_paged_attention_tc(a, m, ws, s);
   return hd <= 64 ? launch_variant<64, false, 4, false>(a, m, ws, s)
                   : hd <= 128 ? launch_variant<128, false, 4, false>(a, m, ws, s)

@@ -574,7 +574,7 @@ cudaError_t launch_dp(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaS
 }  // namespace
 
 int tc_box_keys(const dcu_pages &p) {
-  int box = 16;
+  int box = 8;  // the rows of a swizzle atom
   while (box < kSub && p.page_size % (2 * box) == 0) box *= 2;
   return box;
 }

@@ -322,9 +322,9 @@ bool page_maps(const dcu_pages &p, int kb, PageMaps *m);
 cudaError_t paged_grid(int *grid);  // one range per SM
 cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s);
 
-// k_paged_attn_tc.cu: bf16, boxes of 16 .. 64 slots of one page
+// k_paged_attn_tc.cu: bf16, boxes of 8 .. 64 slots of one page
 constexpr int kTcQueries = 128;  // queries of a tile
-int tc_box_keys(const dcu_pages &p);  // slots of a box (page_size % 16 == 0)
+int tc_box_keys(const dcu_pages &p);  // slots of a box (page_size % 8 == 0)
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaStream_t s);
 
 }  // namespace dcu

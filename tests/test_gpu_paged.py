@@ -383,6 +383,21 @@ def test_paged_attention_keeps_a_bad_query_to_itself(dtype, rows, n):
     assert out[hit].isnan().all() and torch.equal(out[~hit], ref[~hit])
 
 
+@pytest.mark.parametrize("H,KV,hd,page,layout,lens,rows", [
+    (4, 2, 128, 8, "slot", [3001, 0, 63, 65], [130, 3, 9, 40]), (8, 1, 64, 8, "head", [700, 9], [20, 17]),
+    (4, 4, 128, 24, "mixed", [500, 1, 129], [70, 33, 9]), (2, 2, 256, 40, "slot", [333, 64], [65, 20]),
+    (28, 4, 128, 8, "slot", [2000, 31], [2, 30])])
+def test_paged_attention_pages_of_eights(H, KV, hd, page, layout, lens, rows):
+    q, start, lens, table, k, v = case_inputs(90 + page, "bf16", H, KV, hd, page, layout, lens, rows)
+    st = status_word()
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v, status=st)
+    assert st.item() == 0
+    check_attention(out, q, start, lens, table, k, v, "bf16", hd ** -0.5)
+    bad = np.where((np.arange(table.shape[1]) % 5 == 3) & (table >= 0), -1, table).astype(np.int32)
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(bad), k, v, status=st)
+    check_attention(out, q, start, lens, bad, k, v, "bf16", hd ** -0.5)
+
+
 def test_paged_attention_row_starts_outside_the_rows():
     q, start, lens, table, k, v = case_inputs(7, "bf16", 4, 2, 64, 16, "slot", [50, 60], [2, 3], tail=0)
     out = torch.full_like(q, 3.0)
