@@ -38,7 +38,8 @@
 // key with cp.async, 64 x 8192 keys took 289 us instead of 197.  Short calls are a
 // chain of latencies (lengths, table, keys, block, merge): 33 float32 rows over
 // 256 keys of 4 heads 11 us.  float32 blocks of head dim 256 leave room for 4
-// warps only: 2.0 TB/s over 32 x 8192 keys; the other float32 sizes take 4.9.
+// warps only: 2.0 TB/s over 32 x 8192 keys.  float32 head dims up to 128 take 4.9
+// TB/s with 7 queries in the tile, 3.6 with one, whose tile is as much work.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
