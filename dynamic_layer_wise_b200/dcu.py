@@ -470,9 +470,9 @@ def dcu_page_table(lens, page_size: int, max_pages: int, n_pages: int, pool=None
 
 
 def _page_table(raw, lens, p_lens, B, page_size, max_pages, n_pages, p_pool, n_pool, p_first, p_status):
-    table = torch.empty(B, max_pages, dtype=_I32, device=lens.device)
+    table = lens.new_empty(B, max_pages)
     held = torch.empty_like(lens)
-    nxt = torch.empty(1, dtype=_I32, device=lens.device)
+    nxt = lens.new_empty(1)
     _check(lib().dcu_page_table(p_lens, B, page_size, max_pages, n_pages, p_pool, n_pool, p_first, table.data_ptr(),
                                 held.data_ptr(), nxt.data_ptr(), p_status, raw))
     return table, held, nxt
@@ -489,14 +489,14 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
     return _run(dev, stream, _slot_map, (
-        dev, _arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
+        count, _arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
         _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
         _opt(first, "first", _I32, (B,), dev), max_rows, _opt(status, "status", _I32, (1,), dev)))
 
 
-def _slot_map(raw, dev, p_table, B, max_pages, page_size, n_pages, p_count, p_pos, N, p_first, max_rows, p_status):
-    row_start = torch.empty(B + 1, dtype=_I32, device=dev)
-    row_pos = torch.empty(max_rows, dtype=_I32, device=dev)
+def _slot_map(raw, count, p_table, B, max_pages, page_size, n_pages, p_count, p_pos, N, p_first, max_rows, p_status):
+    row_start = count.new_empty(B + 1)
+    row_pos = count.new_empty(max_rows)
     slot = torch.empty_like(row_pos)
     _check(lib().dcu_slot_map(p_table, B, max_pages, page_size, n_pages, p_count, p_pos, N, p_first, max_rows,
                               row_start.data_ptr(), row_pos.data_ptr(), slot.data_ptr(), p_status, raw))
@@ -549,7 +549,7 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
 
 def _paged_write(raw, k_pages, q, p_qkv, T, p_rows, p_pos, p_slot, p_rope, max_pos, n_heads, pages, p_status):
     if q is None:
-        q = torch.empty(T, n_heads, pages.head_dim, dtype=k_pages.dtype, device=k_pages.device)
+        q = k_pages.new_empty(T, n_heads, pages.head_dim)
     _check(lib().dcu_paged_write(p_qkv, T, p_rows, p_pos, p_slot, p_rope, max_pos, n_heads, pages, q.data_ptr(),
                                  p_status, raw))
     return q
