@@ -2,7 +2,8 @@
 // out[r][h] = sum_j w_j V_j, w = softmax_j(scale q . K_j) over the keys j of
 // the row's sequence, read through its block table.  This file: few queries a
 // sequence (one tile of 8), float32, and pages or scales that the tcgen05 kernel
-// of k_paged_attn_tc.cu does not take; and the merge that both share.
+// of k_paged_attn_tc.cu does not take; and the merge that both share (not launched
+// where no item is cut).
 //
 // Work.  A query is a (row, query head) pair; an item is (sequence, kv head,
 // tile of at most R queries), so a tile reads its keys once for the whole GQA
@@ -852,10 +853,12 @@ cudaError_t launch_variant(const PagedAttnArgs &a, const PageMaps &m, void *ws, 
   int grid = 0;
   if (cudaError_t e = paged_grid(&grid)) return e;
   const ShareBuf sb(ws, C::kR, DP);
-  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, a, m.k,
+  PagedAttnArgs b = a;
+  b.whole = whole_items(a, C::kR, C::kKB, 4 * C::kW, grid);
+  if (cudaError_t e = launch_pdl(k_paged_attn<DP, F32, NT, TMA>, dim3(grid), dim3(C::kThreads), C::kSmem, s, b, m.k,
                                  m.v, m.head_first, sb.o, sb.ml, sb.desc))
     return e;
-  return launch_paged_merge(a, C::kR, grid, sb, s);
+  return b.whole ? cudaSuccess : launch_paged_merge(a, C::kR, grid, sb, s);
 }
 
 template <int DP, bool F32, int NT>

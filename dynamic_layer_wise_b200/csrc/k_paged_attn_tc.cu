@@ -565,10 +565,12 @@ cudaError_t launch_dp(const PagedAttnArgs &a, const PageMaps &m, void *ws, cudaS
   int grid = 0;
   if (cudaError_t e = paged_grid(&grid)) return e;
   const ShareBuf sb(ws, kTcQueries, DP);
-  if (cudaError_t e = launch_pdl(k_paged_attn_tc<DP>, dim3(grid), dim3(kThreads), C::kSmem, s, a, m.k, m.v,
+  PagedAttnArgs b = a;
+  b.whole = whole_items(a, kTcQueries, kKC, 4, grid);
+  if (cudaError_t e = launch_pdl(k_paged_attn_tc<DP>, dim3(grid), dim3(kThreads), C::kSmem, s, b, m.k, m.v,
                                  m.head_first, m.box, sb.o, sb.ml, sb.desc))
     return e;
-  return launch_paged_merge(a, kTcQueries, grid, sb, s);
+  return b.whole ? cudaSuccess : launch_paged_merge(a, kTcQueries, grid, sb, s);
 }
 
 }  // namespace

@@ -152,6 +152,7 @@ int dcu_paged_attention(const void *q, int32_t max_rows, const int32_t *row_star
   for (int i = 0; i < 31; ++i)
     if (pages->page_size == 1 << i) a.page_shift = i;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.whole = false;
   a.status = status;
   return pg_cuda(launch_paged_attention(a, workspace, (cudaStream_t)stream), "dcu_paged_attention");
 }

@@ -31,6 +31,7 @@ struct PagedAttnArgs {
   int32_t B, max_rows, max_pages, n_heads;
   int32_t page_shift;  // log2(page_size), -1 when it is no power of two
   float scale_log2;    // scale * log2(e)
+  bool whole;          // no item is cut: fewer items than CTAs, and short ones (whole_items)
   int32_t *status;
 };
 int64_t paged_attention_workspace(const dcu_pages &pages);

@@ -148,8 +148,8 @@ __device__ __forceinline__ void find_range(const PagedAttnArgs &a, Place *place,
     const int ranges = (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least)));
     cut_even(rg, total, ranges);
     if (total > 0 && items <= ranges) {
-      const int f = ranges / (int)items;
-      if ((p.s.nblk + f - 1) / f <= (int)rg.q + (rg.rem ? 1 : 0) + turn) {
+      const int f = a.whole ? 1 : ranges / (int)items;
+      if (a.whole || (p.s.nblk + f - 1) / f <= (int)rg.q + (rg.rem ? 1 : 0) + turn) {
         const int item = (int)blockIdx.x / f;
         rg.any = item < items;
         if (rg.any) cut_item(rg, p, item, (int)blockIdx.x - item * f, f, item * f);
@@ -201,7 +201,7 @@ __device__ __forceinline__ void find_range(const PagedAttnArgs &a, Place *place,
     // items + total / cut, below 300) are added up packed, 16 bits for each c.
     constexpr int NC = 4;
     __shared__ unsigned long long s_cnt[W];
-    const int even = (int)div_ll(total + ranges - 1, ranges);
+    const int even = a.whole ? 1 << 30 : (int)div_ll(total + ranges - 1, ranges);
     const int cut[NC] = {even, even + turn / 4, even + turn / 2, even + turn};
     unsigned long long n = 0;
     for (int b = b0; b < b1; ++b) {
@@ -320,6 +320,16 @@ struct PageMaps {
 // k_paged_attn.cu
 bool page_maps(const dcu_pages &p, int kb, PageMaps *m);
 cudaError_t paged_grid(int *grid);  // one range per SM
+// Whether no item of a call is to be cut, which spares the merge: at most `most` units of kb keys an item, by what the
+// table holds, and not more tiles of r queries than CTAs, by the rows and sequences.  Measured with 4 units (narrow
+// kernel: 4 blocks a warp), cut / whole, us in a graph: 65 rows of 32 heads x 512 keys 14.3 / 11.8, one row x 256 keys
+// 9.5 / 6.8, 33 float32 rows of 4 heads x 256 keys 11.1 / 9.6 (2.2 us less from Python in each case); with 8 units 65
+// rows x 1024 keys 15.2 / 15.8, one row x 1024 keys 10.9 / 12.8.
+inline bool whole_items(const PagedAttnArgs &a, int r, int kb, int most, int grid) {
+  const long long q = (long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads);
+  return (long long)a.max_pages * a.pages.page_size <= (long long)kb * most &&
+         ((q + r - 1) / r + a.B - 1) * a.pages.n_kv_heads <= grid;
+}
 cudaError_t launch_paged_merge(const PagedAttnArgs &a, int kr, int grid, const ShareBuf &sb, cudaStream_t s);
 
 // k_paged_attn_tc.cu: bf16, boxes of 8 .. 64 slots of one page

@@ -398,6 +398,23 @@ def test_paged_attention_pages_of_eights(H, KV, hd, page, layout, lens, rows):
     check_attention(out, q, start, lens, bad, k, v, "bf16", hd ** -0.5)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,KV,hd,page,lens,rows", [(32, 32, 128, 16, [512], [65]), (4, 4, 64, 16, [256], [33]),
+                                                    (8, 2, 128, 64, [250, 0, 1, 129], [1, 2, 1, 1]),
+                                                    (4, 2, 256, 16, [60, 33], [40, 7]), (28, 4, 128, 8, [384], [1])])
+def test_paged_attention_short_and_wide_tables(dtype, H, KV, hd, page, lens, rows):
+    """What a table could hold decides whether items are cut; the keys there are decide the result."""
+    q, start, lens, table, k, v = case_inputs(95, dtype, H, KV, hd, page, "slot", lens, rows)
+    wide = np.full((len(lens), 5000), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    for tab in (table, wide):
+        st = status_word()
+        out = torch.full_like(q, 3.0)
+        dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(tab), k, v, out=out, status=st)
+        assert st.item() == 0 and (out[int(start[-1]):] == 3.0).all()
+        check_attention(out, q, start, lens, tab, k, v, dtype, hd ** -0.5)
+
+
 def test_paged_attention_row_starts_outside_the_rows():
     q, start, lens, table, k, v = case_inputs(7, "bf16", 4, 2, 64, 16, "slot", [50, 60], [2, 3], tail=0)
     out = torch.full_like(q, 3.0)
