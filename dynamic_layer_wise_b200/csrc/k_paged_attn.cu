@@ -37,8 +37,8 @@
 // 64 ragged sequences (1.06 GB) 189 us, 5.6 TB/s; one of 131072 keys (268 MB)
 // 52.6 us, 5.1 TB/s.  The rings hold 192 KB an SM, 28 MB on the GPU; loaded key by
 // key with cp.async, 64 x 8192 keys took 289 us instead of 197.  Short calls are a
-// chain of latencies (lengths, table, keys, block, merge): 33 float32 rows over
-// 256 keys of 4 heads 11 us.  float32 blocks of head dim 256 leave room for 4
+// chain of latencies (lengths, table, keys, blocks, joins): 33 float32 rows over
+// 256 keys of 4 heads 9.7 us.  float32 blocks of head dim 256 leave room for 4
 // warps only: 2.0 TB/s over 32 x 8192 keys.  float32 head dims up to 128 take 4.9
 // TB/s with 7 queries in the tile, 3.6 with one, whose tile is as much work.
 #include "paged_attn.cuh"
