@@ -503,6 +503,53 @@ def test_another_stream_and_two_calls_at_once():
         assert all(torch.equal(o[:n], want[i][:n]) for o in got[i])
 
 
+def test_many_rows_on_far_pages():
+    """The tensor-core path over pages whose elements lie beyond 2^31 elements and 2^32 bytes."""
+    n_pages, page, KV, hd = 70000, 64, 4, 128
+    k = torch.zeros((n_pages, page, KV, hd), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    far = [69999, 3, 69998, 40000, 66000]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for p in far:
+        k[p], v[p] = (torch.randn((page, KV, hd), generator=g, device="cuda").to(k.dtype) for _ in range(2))
+    q = torch.randn((90, 8, hd), generator=g, device="cuda").to(k.dtype)
+    out = dcu.dcu_paged_attention(q, i32([0, 90]), i32([300]), i32([far]), k, v)
+    idx = torch.tensor(far, device="cuda")
+    small = dcu.dcu_paged_attention(q, i32([0, 90]), i32([300]), i32([[0, 1, 2, 3, 4]]), k[idx], v[idx])
+    assert torch.equal(out, small) and out.abs().max() > 0
+
+
+def test_many_rows_replayed_and_on_two_streams():
+    """The tensor-core path in a captured call over changing lengths and rows, and two calls at once."""
+    H, KV, hd, page, B, cap = 8, 2, 128, 16, 5, 400
+    rng = np.random.default_rng(21)
+    k, v = make_pages(22, 600, page, KV, hd, torch.bfloat16, "slot")
+    g = torch.Generator(device="cuda").manual_seed(23)
+    q = torch.randn((cap, H, hd), generator=g, device="cuda").to(k.dtype)
+    start, lens = i32(np.zeros(B + 1)), i32(np.zeros(B))
+    table = i32(rng.permutation(600)[:B * 120].reshape(B, 120))
+    ws = torch.empty(dcu.dcu_paged_attention_workspace(k, v), dtype=torch.uint8, device="cuda")
+    dcu.dcu_paged_attention(q, start, lens, table, k, v, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dcu.dcu_paged_attention(q, start, lens, table, k, v, workspace=ws)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for trial in range(4):
+        rows = rng.integers(0, 80, B)
+        lens.copy_(i32(rng.integers(0, 1921, B))), start.copy_(i32(np.concatenate([[0], np.cumsum(rows)])))
+        T = int(rows.sum())
+        out.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (out[T:] == 3.0).all()
+        check_attention(out, q, f64(start).astype(int), f64(lens).astype(int), f64(table).astype(int), k, v, "bf16",
+                        hd ** -0.5)
+        got = [dcu.dcu_paged_attention(q, start, lens, table, k, v, stream=s) for s in streams * 4]
+        torch.cuda.synchronize()
+        assert all(torch.equal(o[:T], out[:T]) for o in got)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_layers_attention_run_together(dtype):
     """Token selection, slots, QKV product, RoPE + write, attention and the O product over pages, as a step runs
