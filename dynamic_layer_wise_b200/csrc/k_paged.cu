@@ -204,23 +204,28 @@ __global__ void __launch_bounds__(kMapThreads)
 }
 
 // ------------------------------------------------------------------ RoPE + K/V write
-// A work item is 8 pairs of one q or k head (elements j .. j + 7 of both
-// halves) or 16 consecutive v elements: 64 bytes read, two vectors written.
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// A work item is elements j .. j + 3 of both halves of a head (4 pairs of q or k;
+// of v merely 8 elements): 32 bytes read, two vectors written, and a warp's loads
+// and stores are whole lines.  (Items of 8 pairs, whose lanes read every other 16
+// bytes, measured before: 1.03 to 1.09 times as long in bf16, 1.1 to 1.17 in
+// float32, 1.4 for 512 rows in L2.)
+__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
 }
-__device__ __forceinline__ void store8(bf16 *p, const float (&v)[8]) { store_vec<bf16>(p, v); }
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store4(bf16 *p, const float (&v)[4]) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
+  *reinterpret_cast<uint2 *>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+}
+__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// grid (rows, slices of a row): each thread has one item of one row, and its 64
+// grid (rows, slices of a row): each thread has one item of one row, and its 32
 // bytes are on the way before the row's slot and position are known.  A row is
 // streamed once and written once, so memory bounds it: 6148 rows of 28 + 2 x 4
-// heads of 128 take 31.3 us, 5.5 TB/s (a plain copy: 6.46); 65 rows of 96 heads
+// heads of 128 take 28.7 us, 6.0 TB/s (a plain copy: 6.46); 65 rows of 96 heads
 // 2.3 us, a launch.  q, K and V are rounded once, from the fp32 rotation.
 constexpr int kWriteMax = 512;  // most threads of a CTA
 
@@ -232,18 +237,15 @@ __global__ void __launch_bounds__(kWriteMax)
                   int32_t *status) {
   pdl_enter();
   const int hd = pg.head_dim, KV = pg.n_kv_heads, half = hd / 2;
-  const int n_rope = (H + KV) * (half / 8), items = n_rope + KV * (hd / 16);
+  const int per = half / 4, items = (H + 2 * KV) * per;
   const int t = blockIdx.x, u = blockIdx.y * blockDim.x + threadIdx.x;
   if (u >= items) return;
-  // element offsets of the item's two vectors of 8 in the row
-  const bool is_v = u >= n_rope;
-  const int per = is_v ? hd / 16 : half / 8, head = (is_v ? u - n_rope : u) / per;
-  const int j = ((is_v ? u - n_rope : u) - head * per) * (is_v ? 16 : 8);
-  const int second = is_v ? 8 : half;
-  const float *x = qkv + (size_t)t * (size_t)(H + 2 * KV) * hd + (size_t)(is_v ? H + KV + head : head) * hd + j;
-  float a[8], b[8];
-  load8(x, a);
-  load8(x + second, b);
+  const int head = u / per, j = (u - head * per) * 4;
+  const bool is_v = head >= H + KV;
+  const float *x = qkv + (size_t)t * (size_t)(H + 2 * KV) * hd + (size_t)head * hd + j;
+  float a[4], b[4];
+  load4(x, a);
+  load4(x + half, b);
   const int sl = slot[t], p = rope ? row_pos[t] : 0, used = n_rows ? *n_rows : max_rows;
   if (t >= used) return;
   const long long n_slots = (long long)pg.n_pages * pg.page_size;
@@ -253,18 +255,18 @@ __global__ void __launch_bounds__(kWriteMax)
     if (sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
   }
   T *dst;
-  if (!is_v && head < H) {
+  if (head < H) {
     dst = q + ((size_t)t * H + head) * hd + j;
   } else {
     if (!good || sl < 0 || sl >= n_slots) return;
     const int page = (int)((unsigned)sl / (unsigned)pg.page_size);
     dst = static_cast<T *>(is_v ? pg.v : pg.k) + (int64_t)page * pg.page_stride +
-          (int64_t)(sl - page * pg.page_size) * pg.slot_stride + (int64_t)(is_v ? head : head - H) * pg.head_stride + j;
+          (int64_t)(sl - page * pg.page_size) * pg.slot_stride + (int64_t)(head - H - (is_v ? KV : 0)) * pg.head_stride + j;
   }
   if (rope && !is_v) {
     const float4 *cs = reinterpret_cast<const float4 *>(rope + (size_t)(good ? p : 0) * half + j);
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < 4; e += 2) {
       const float4 c = __ldg(cs + e / 2);
       const float a0 = a[e] * c.x - b[e] * c.y, b0 = b[e] * c.x + a[e] * c.y;
       const float a1 = a[e + 1] * c.z - b[e + 1] * c.w, b1 = b[e + 1] * c.z + a[e + 1] * c.w;
@@ -274,8 +276,8 @@ __global__ void __launch_bounds__(kWriteMax)
       b[e + 1] = good ? b1 : 0.f;
     }
   }
-  store8(dst, a);
-  store8(dst + second, b);
+  store4(dst, a);
+  store4(dst + half, b);
 }
 
 }  // namespace
@@ -304,7 +306,7 @@ cudaError_t launch_paged_write(const float *qkv, int max_rows, const int32_t *n_
                                const int32_t *slot, const float2 *rope, int max_pos, int n_heads,
                                const dcu_pages &pages, void *q, int32_t *status, cudaStream_t s) {
   // a row's items in as few slices as fit a CTA, in equal parts
-  const int items = (n_heads + 2 * pages.n_kv_heads) * (pages.head_dim / 16);
+  const int items = (n_heads + 2 * pages.n_kv_heads) * (pages.head_dim / 8);
   const int slices = (items + kWriteMax - 1) / kWriteMax;
   const int threads = ((items + slices - 1) / slices + 31) / 32 * 32;
   const dim3 grid(max_rows, slices);

@@ -98,7 +98,7 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
     return pg_fail(DCU_EINVAL, "dcu_paged_write: bad argument");
   if (mis(qkv, 16) || mis(rope, 16) || mis(q, 16))
     return pg_fail(DCU_EINVAL, "dcu_paged_write: qkv, rope and q must be 16-byte aligned");
-  if ((int64_t)n_heads + 2ll * pages->n_kv_heads > (1ll << 20))
+  if ((int64_t)n_heads + 2ll * pages->n_kv_heads > (1ll << 19))  // (32 items a head, 512 a block, 65535 slices)
     return pg_fail(DCU_EINVAL, "dcu_paged_write: too many heads");
   if ((pages->n_pages > 1 && !pages->page_stride) || (pages->page_size > 1 && !pages->slot_stride) ||
       (pages->n_kv_heads > 1 && !pages->head_stride))

@@ -413,7 +413,8 @@ int dcu_rope_table(float *tab, int32_t max_pos, int32_t head_dim, float theta, d
  * row_pos outside [0, max_pos) gives a zero query and no K/V write
  * (DCU_ST_BAD_ROW; not looked at without rope).  Strides must be positive where
  * their dimension is above 1, no two slots may overlap, K and V are two arrays, and
- * q may not overlap qkv.  Two rows with the same slot leave a mixture of both there. */
+ * q may not overlap qkv.  Two rows with the same slot leave a mixture of both there.
+ * n_heads + 2 n_kv_heads <= 2^19. */
 int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, const int32_t *row_pos,
                     const int32_t *slot, const float *rope, int32_t max_pos, int32_t n_heads,
                     const dcu_pages *pages, void *q, int32_t *status, dcu_stream_t stream);

@@ -126,3 +126,6 @@ def test_sizes_and_overlaps_that_are_refused(L):
     assert b"overlaps" in L.dcu_last_error(None)
     assert _call(L.dcu_paged_write, WRITE, q=1 << 30) == dcu.DCU_EINVAL
     assert b"share" in L.dcu_last_error(None)
+    # 32 items a head of 256 dims, 512 a block, 65535 slices of a row
+    assert _call(L.dcu_paged_write, WRITE, n_heads=(1 << 19) - 7) == dcu.DCU_EINVAL
+    assert b"heads" in L.dcu_last_error(None)
