@@ -486,6 +486,8 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
     B, max_pages = _dims(table, "table", 2)
     dev = table.device
     N = 0 if pos is None else _dims(pos, "pos", 2)[1]
+    if pos is not None and not N:  # its address is NULL, which the library takes for no positions
+        raise ValueError("pos: expected at least one column")
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
     return _run(dev, stream, _slot_map, (
@@ -537,6 +539,8 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
     if n_start < 1:
         raise ValueError("row_start: expected at least one entry")
     max_pos = 0 if rope is None else _dims(rope, "rope", 3)[0]
+    if rope is not None and not max_pos:  # its address is NULL, which the library takes for no rotation
+        raise ValueError("rope: expected at least one position")
     if q is not None:
         _arg(q, "q", k_pages.dtype, (T, n_heads, hd), dev)
     return _run(dev, stream, _paged_write, (

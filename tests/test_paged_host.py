@@ -129,3 +129,13 @@ def test_sizes_and_overlaps_that_are_refused(L):
     # 32 items a head of 256 dims, 512 a block, 65535 slices of a row
     assert _call(L.dcu_paged_write, WRITE, n_heads=(1 << 19) - 7) == dcu.DCU_EINVAL
     assert b"heads" in L.dcu_last_error(None)
+
+
+def test_binding_refuses_empty_tensors_that_would_pass_for_none(L):
+    """An empty tensor has no address, and without one the library counts positions from 0 and rotates nothing."""
+    i = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="pos: expected at least one column"):
+        dcu.dcu_slot_map(i[None], i[:1], 16, 8, 4, pos=torch.zeros(1, 0, dtype=torch.int32))
+    k = torch.zeros(2, 16, 4, 64)
+    with pytest.raises(ValueError, match="rope: expected at least one position"):
+        dcu.dcu_paged_write(torch.zeros(4, 1024), i, i, i, torch.zeros(0, 32, 2), k, k, 8)
