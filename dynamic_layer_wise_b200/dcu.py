@@ -437,6 +437,12 @@ def _dims(t, name: str, n: int):
     return t.shape
 
 
+def _sizes(bits: int):
+    """Refuses sizes, OR-ed together, of which one is above 2^31 - 1: ctypes would pass its low 32 bits."""
+    if bits > 0x7fffffff:
+        raise ValueError("sizes above 2^31 - 1 are not supported")
+
+
 def _pages(k_pages, v_pages, device) -> dcu_pages:
     """dcu_pages of K and V tensors [n_pages][page_size][n_kv_heads][head_dim] (any strides but the last)."""
     n, p, h, d = shape = _dims(k_pages, "k_pages", 4)
@@ -450,6 +456,7 @@ def _pages(k_pages, v_pages, device) -> dcu_pages:
     if (sd != 1 and d != 1) or 0 in shape:
         raise ValueError(f"k_pages: expected [n_pages][page_size][n_kv_heads][head_dim] with a contiguous last "
                          f"dimension, got {tuple(shape)} with strides {strides}")
+    _sizes(n | p | h | d)
     return dcu_pages(k_pages.data_ptr(), v_pages.data_ptr(), sn if n > 1 else 0, sp if p > 1 else 0,
                      sh if h > 1 else 0, n, p, h, d, _DTYPE_CODE[k_pages.dtype])
 
@@ -463,6 +470,7 @@ def dcu_page_table(lens, page_size: int, max_pages: int, n_pages: int, pool=None
     n_pool = n_pages if pool is None else _dims(pool, "pool", 1)[0]
     if max_pages <= 0:
         raise ValueError("max_pages must be positive")
+    _sizes(B | page_size | max_pages | n_pages | n_pool)
     return _run(dev, stream, _page_table, (
         lens, _arg(lens, "lens", _I32, (B,), dev), B, page_size, max_pages, n_pages,
         _opt(pool, "pool", _I32, (n_pool,), dev), n_pool, _opt(first, "first", _I32, (1,), dev),
@@ -490,6 +498,7 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
         raise ValueError("pos: expected at least one column")
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
+    _sizes(B | max_pages | page_size | n_pages | N | max_rows)
     return _run(dev, stream, _slot_map, (
         count, _arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
         _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
@@ -509,6 +518,7 @@ def dcu_rope_table(max_pos: int, head_dim: int, theta: float = 10000.0, device="
     """(cos, sin) of pos * theta^(-2j / head_dim): float32 [max_pos][head_dim / 2][2]."""
     if max_pos <= 0 or head_dim <= 0 or head_dim % 2:
         raise ValueError("max_pos and head_dim must be positive, head_dim even")
+    _sizes(max_pos | head_dim)
     dev = torch.device(device)
     if dev.type != "cuda":
         raise ValueError("expected a CUDA device")
@@ -541,6 +551,7 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
     max_pos = 0 if rope is None else _dims(rope, "rope", 3)[0]
     if rope is not None and not max_pos:  # its address is NULL, which the library takes for no rotation
         raise ValueError("rope: expected at least one position")
+    _sizes(T | max_pos | n_heads)
     if q is not None:
         _arg(q, "q", k_pages.dtype, (T, n_heads, hd), dev)
     return _run(dev, stream, _paged_write, (
@@ -570,6 +581,7 @@ def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: fl
     dev = q.device
     pages = _pages(k_pages, v_pages, dev)
     B, max_pages = _dims(table, "table", 2)
+    _sizes(T | H | B | max_pages)
     if out is not None:
         _arg(out, "out", q.dtype, (T, H, hd), dev)
     if workspace is not None:

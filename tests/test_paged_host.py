@@ -139,3 +139,19 @@ def test_binding_refuses_empty_tensors_that_would_pass_for_none(L):
     k = torch.zeros(2, 16, 4, 64)
     with pytest.raises(ValueError, match="rope: expected at least one position"):
         dcu.dcu_paged_write(torch.zeros(4, 1024), i, i, i, torch.zeros(0, 32, 2), k, k, 8)
+
+
+@pytest.mark.parametrize("call", [
+    lambda i, k: dcu.dcu_page_table(i, (1 << 32) + 16, 4, 8), lambda i, k: dcu.dcu_page_table(i, 16, (1 << 32) + 4, 8),
+    lambda i, k: dcu.dcu_page_table(i, 16, 4, (1 << 32) + 8), lambda i, k: dcu.dcu_slot_map(i[None], i[:1], 1 << 32, 8, 4),
+    lambda i, k: dcu.dcu_slot_map(i[None], i[:1], 16, (1 << 32) + 8, 4),
+    lambda i, k: dcu.dcu_slot_map(i[None], i[:1], 16, 8, 1 << 31),
+    lambda i, k: dcu.dcu_rope_table((1 << 32) + 8, 64, device="cuda:0"),
+    lambda i, k: dcu.dcu_rope_table(8, 1 << 32, device="cuda:0"),
+    lambda i, k: dcu.dcu_slot_map(i[None], i[:1], 16, 8, 4, pos=i[:1].expand(1, (1 << 32) + 2)),
+    lambda i, k: dcu.dcu_paged_attention(k[0, :3], i, i, i[:1].expand(1, (1 << 32) + 2), k, k),
+    lambda i, k: dcu.dcu_paged_attention(k[0, :3], i, i, i[None], *[k[:, :1].expand(2, (1 << 32) + 1, 4, 64)] * 2)])
+def test_binding_refuses_sizes_past_32_bits(L, call):
+    """ctypes keeps the low 32 bits of an integer: 2^32 + 16 would become 16."""
+    with pytest.raises(ValueError, match="sizes above"):
+        call(torch.zeros(4, dtype=torch.int32), torch.zeros(2, 16, 4, 64))
