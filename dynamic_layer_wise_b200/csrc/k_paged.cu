@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kWriteMax)
   const bool good = !rope || (p >= 0 && p < max_pos);
   if (u == 0) {
     if (!good) flag(status, DCU_ST_BAD_ROW);
-    if (sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
+    if (sl < -1 || sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
   }
   T *dst;
   if (head < H) {

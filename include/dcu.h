@@ -409,7 +409,8 @@ int dcu_rope_table(float *tab, int32_t max_pos, int32_t head_dim, float theta, d
  * int32, the rows in use (row_start + B; NULL: max_rows).  q (dev [max_rows][n_heads][head_dim]
  * in the pages' dtype) gets the rotated queries; K (rotated) and V go to the
  * row's slot.  rope: the table of dcu_rope_table, NULL for no rotation.  A slot
- * outside [0, n_pages * page_size) is not written (a slot of -1 silently).  A
+ * outside [0, n_pages * page_size) is not written (DCU_ST_BAD_PAGE, but for the -1
+ * of a position without a page, which dcu_slot_map has flagged).  A
  * row_pos outside [0, max_pos) gives a zero query and no K/V write
  * (DCU_ST_BAD_ROW; not looked at without rope).  Strides must be positive where
  * their dimension is above 1, no two slots may overlap, K and V are two arrays, and

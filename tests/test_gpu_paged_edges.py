@@ -1,0 +1,32 @@
+"""Calls of the paged K/V cache operators at the edges of what their documentation allows: what is flagged, and
+batches of many sequences."""
+import numpy as np
+import pytest
+import torch
+
+from dynamic_layer_wise_b200 import dcu
+from tests import paged_ref as R
+from tests.test_gpu_paged import DT, i32, make_pages, status_word
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ RoPE + K/V write
+
+@pytest.mark.parametrize("slot,flag", [(-1, 0), (-2, R.BAD_PAGE), (-2 ** 31, R.BAD_PAGE), (64, R.BAD_PAGE),
+                                       (2 ** 31 - 1, R.BAD_PAGE), (63, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_write_flags_slots_outside_the_pages(dtype, slot, flag):
+    H, KV, hd = 4, 2, 16
+    k, v = make_pages(1, 4, 16, KV, hd, DT[dtype], "slot")
+    k0, v0 = k.clone(), v.clone()
+    qkv = torch.randn((3, (H + 2 * KV) * hd), device="cuda")
+    st = status_word()
+    q = dcu.dcu_paged_write(qkv, i32([0, 3]), i32([0, 1, 2]), i32([5, slot, 6]), None, k, v, H, status=st)
+    assert st.item() == flag
+    x = qkv.view(3, H + 2 * KV, hd).to(DT[dtype])
+    assert torch.equal(q, x[:, :H])
+    for t, s in enumerate([5, slot, 6]):
+        if 0 <= s < 64:
+            k0[s // 16, s % 16], v0[s // 16, s % 16] = x[t, H:H + KV], x[t, H + KV:]
+    assert torch.equal(k, k0) and torch.equal(v, v0)
