@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kWriteMax)
   const long long n_slots = (long long)pg.n_pages * pg.page_size;
   const bool good = !rope || (p >= 0 && p < max_pos);
   if (u == 0) {
-    if (!good) flag(status, DCU_ST_BAD_ROW);
+    if (!good || (t == 0 && used > max_rows)) flag(status, DCU_ST_BAD_ROW);
     if (sl < -1 || sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
   }
   T *dst;

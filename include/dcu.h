@@ -406,7 +406,8 @@ int dcu_rope_table(float *tab, int32_t max_pos, int32_t head_dim, float theta, d
 /* RoPE and the paged K/V write of packed rows: the QKV epilogue of a layer.
  * qkv: dev float [max_rows][(n_heads + 2 n_kv_heads) * head_dim] (q heads, k
  * heads, v heads; the output of dcu_linear over stacked wq, wk, wv); n_rows: dev
- * int32, the rows in use (row_start + B; NULL: max_rows).  q (dev [max_rows][n_heads][head_dim]
+ * int32, the rows in use (row_start + B; NULL: max_rows; more than max_rows:
+ * DCU_ST_BAD_ROW, the first max_rows are written).  q (dev [max_rows][n_heads][head_dim]
  * in the pages' dtype) gets the rotated queries; K (rotated) and V go to the
  * row's slot.  rope: the table of dcu_rope_table, NULL for no rotation.  A slot
  * outside [0, n_pages * page_size) is not written (DCU_ST_BAD_PAGE, but for the -1

@@ -30,3 +30,15 @@ def test_paged_write_flags_slots_outside_the_pages(dtype, slot, flag):
         if 0 <= s < 64:
             k0[s // 16, s % 16], v0[s // 16, s % 16] = x[t, H:H + KV], x[t, H + KV:]
     assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
+@pytest.mark.parametrize("used,flag", [(6, R.BAD_ROW), (2 ** 31 - 1, R.BAD_ROW), (5, 0), (0, 0), (-3, 0)])
+def test_paged_write_flags_more_rows_than_there_are(used, flag):
+    H, KV, hd = 4, 2, 16
+    k, v = make_pages(2, 4, 16, KV, hd, torch.bfloat16, "slot")
+    qkv = torch.randn((5, (H + 2 * KV) * hd), device="cuda")
+    st = status_word()
+    q = torch.full((5, H, hd), 7.0, dtype=k.dtype, device="cuda")
+    dcu.dcu_paged_write(qkv, i32([0, used]), i32(range(5)), i32(range(5)), None, k, v, H, q=q, status=st)
+    n = max(0, min(used, 5))
+    assert st.item() == flag and torch.equal(q[:n], qkv.view(5, -1, hd)[:n, :H].to(k.dtype)) and (q[n:] == 7.0).all()
