@@ -36,7 +36,9 @@ struct Seq {
 template <int R, int KB>
 __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   Seq s;
-  const int lo = min(max(a.row_start[b], 0), a.max_rows), hi = min(max(a.row_start[b + 1], 0), a.max_rows);
+  const int r0 = a.row_start[b], r1 = a.row_start[b + 1];
+  if ((r0 < 0 || r1 < r0 || r1 > a.max_rows) && a.status) atomicOr(a.status, DCU_ST_BAD_ROW);
+  const int lo = min(max(r0, 0), a.max_rows), hi = min(max(r1, 0), a.max_rows);
   const int rows = max(hi - lo, 0);
   s.row0 = lo;
   s.nq = rows * (a.n_heads / a.pages.n_kv_heads);

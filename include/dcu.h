@@ -429,6 +429,10 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
  * [B]; table: dev int32 [B][max_pages]; out may not overlap q.  Slots at and past kv_len are never
  * used, whatever they hold; keys on a page outside [0, n_pages) or past the
  * table row are left out (DCU_ST_BAD_PAGE); a row with no key gives zeros.
+ * Row starts outside [0, max_rows] are taken as the nearer end, and a sequence
+ * whose row start lies above the next one has no rows (DCU_ST_BAD_ROW for both);
+ * where row starts decrease, rows may belong to two sequences, and what out holds
+ * in the rows that any sequence covers is unspecified.
  * The keys are split over the SMs and joined in a fixed order: equal inputs
  * give equal bits.  workspace: dev, 16-byte aligned, at least
  * dcu_paged_attention_workspace bytes, any content; calls that may overlap (on

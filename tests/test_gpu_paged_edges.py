@@ -6,7 +6,7 @@ import torch
 
 from dynamic_layer_wise_b200 import dcu
 from tests import paged_ref as R
-from tests.test_gpu_paged import DT, i32, make_pages, status_word
+from tests.test_gpu_paged import DT, case_inputs, i32, make_pages, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,33 @@ def test_paged_write_flags_more_rows_than_there_are(used, flag):
     dcu.dcu_paged_write(qkv, i32([0, used]), i32(range(5)), i32(range(5)), None, k, v, H, q=q, status=st)
     n = max(0, min(used, 5))
     assert st.item() == flag and torch.equal(q[:n], qkv.view(5, -1, hd)[:n, :H].to(k.dtype)) and (q[n:] == 7.0).all()
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 40), ("f32", 9)])
+def test_paged_attention_flags_row_starts_out_of_order_or_range(dtype, rows):
+    q, start, lens, table, k, v = case_inputs(7, dtype, 4, 2, 64, 16, "slot", [50, 60, 33], [rows] * 3, tail=3)
+    T = 3 * rows
+
+    def call(s, max_rows=T + 3):
+        st, out = status_word(), torch.full_like(q[:max_rows], 3.0)
+        dcu.dcu_paged_attention(q[:max_rows], i32(s), i32(lens), i32(table), k, v, out=out, status=st)
+        return st.item(), out
+
+    flag, ref = call(start)
+    assert flag == 0 and (ref[T:] == 3.0).all()
+    # outside the rows: taken as the nearer end
+    flag, out = call([-4, rows, 2 * rows, T])
+    assert flag == R.BAD_ROW and torch.equal(out, ref)
+    flag, out = call([0, rows, 2 * rows, T + 1], T)
+    assert flag == R.BAD_ROW and torch.equal(out, ref[:T])
+    flag, out = call([0, rows, 2 ** 31 - 1, 2 ** 31 - 1], 2 * rows)
+    assert flag == R.BAD_ROW and torch.equal(out[:rows], ref[:rows])
+    # out of order: rows that no sequence covers stay as they were
+    for s in ([0, rows + 1, rows, 2 * rows], [0, 2 * rows, 0, rows], [rows, 0, 0, 0], [2, 1, 1, 2]):
+        flag, out = call(s)
+        covered = torch.zeros(T + 3, dtype=torch.bool)
+        for a, z in zip(s, s[1:]):
+            covered[a:z] = True
+        assert flag == R.BAD_ROW and (out[~covered.cuda()] == 3.0).all()
