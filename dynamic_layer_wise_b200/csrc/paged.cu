@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <string>
 
 #include "kernels.h"
@@ -35,6 +36,22 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
+struct Span {
+  const void *p;  // NULL: not given
+  int64_t bytes;
+};
+// Whether an output overlaps an input or another output: the kernels' threads read and write in no order.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+    if (!o->p || !o->bytes) continue;
+    for (const Span *x = outs.begin(); x != o; ++x)
+      if (x->p && x->bytes && overlap(o->p, o->bytes, x->p, x->bytes)) return true;
+    for (const Span &x : ins)
+      if (x.p && x.bytes && overlap(o->p, o->bytes, x.p, x.bytes)) return true;
+  }
+  return false;
+}
+
 bool mis(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 const char *bad_pages(const dcu_pages *p) {
@@ -64,6 +81,9 @@ int dcu_page_table(const int32_t *lens, int32_t B, int32_t page_size, int32_t ma
     return pg_fail(DCU_EINVAL, "dcu_page_table: bad argument");
   if (!pool && n_pool != n_pages && n_pool != 0)
     return pg_fail(DCU_EINVAL, "dcu_page_table: without a pool, n_pool must be n_pages");
+  if (clash({{table, 4ll * B * max_pages}, {held, 4ll * B}, {next, 4}, {status, 4}},
+            {{lens, 4ll * B}, {pool, 4ll * n_pool}, {first, 4}}))
+    return pg_fail(DCU_EINVAL, "dcu_page_table: an output overlaps another array");
   return pg_cuda(launch_page_table(lens, B, page_size, max_pages, n_pages, pool, n_pool, first, table, held, next,
                                    status, (cudaStream_t)stream),
                  "dcu_page_table");
@@ -77,6 +97,9 @@ int dcu_slot_map(const int32_t *table, int32_t B, int32_t max_pages, int32_t pag
       n_pages <= 0 || (int64_t)n_pages * page_size >= (1ll << 31) || max_rows < 0 ||
       (max_rows > 0 && (!row_pos || !slot)) || (pos && (pos_stride <= 0 || first)))
     return pg_fail(DCU_EINVAL, "dcu_slot_map: bad argument");
+  if (clash({{row_start, 4ll * (B + 1)}, {row_pos, 4ll * max_rows}, {slot, 4ll * max_rows}, {status, 4}},
+            {{table, 4ll * B * max_pages}, {count, 4ll * B}, {pos, 4ll * B * pos_stride}, {first, 4ll * B}}))
+    return pg_fail(DCU_EINVAL, "dcu_slot_map: an output overlaps another array");
   return pg_cuda(launch_slot_map(table, B, max_pages, page_size, n_pages, count, pos, pos_stride, first, max_rows,
                                  row_start, row_pos, slot, status, (cudaStream_t)stream),
                  "dcu_slot_map");
@@ -108,6 +131,9 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
   const int64_t es = pages->dtype == DCU_BF16 ? 2 : 4, rh = (int64_t)max_rows * pages->head_dim;
   if (overlap(q, rh * n_heads * es, qkv, rh * (n_heads + 2ll * pages->n_kv_heads) * 4))
     return pg_fail(DCU_EINVAL, "dcu_paged_write: q overlaps qkv");
+  if (clash({{q, rh * n_heads * es}, {status, 4}},
+            {{n_rows, 4}, {row_pos, 4ll * max_rows}, {slot, 4ll * max_rows}, {rope, rope ? 4ll * max_pos * pages->head_dim : 0}}))
+    return pg_fail(DCU_EINVAL, "dcu_paged_write: q overlaps another array");
   return pg_cuda(launch_paged_write(qkv, max_rows, n_rows, row_pos, slot, reinterpret_cast<const float2 *>(rope),
                                     max_pos, n_heads, *pages, q, status, (cudaStream_t)stream),
                  "dcu_paged_write");
@@ -137,6 +163,9 @@ int dcu_paged_attention(const void *q, int32_t max_rows, const int32_t *row_star
   if (overlap(q, qb, out, qb)) return pg_fail(DCU_EINVAL, "dcu_paged_attention: out may not overlap q");
   if (!workspace || workspace_bytes < paged_attention_workspace(*pages))
     return pg_fail(DCU_EINVAL, "dcu_paged_attention: workspace smaller than dcu_paged_attention_workspace");
+  if (clash({{out, qb}, {workspace, paged_attention_workspace(*pages)}, {status, 4}},
+            {{q, qb}, {row_start, 4ll * (B + 1)}, {kv_len, 4ll * B}, {table, 4ll * B * max_pages}}))
+    return pg_fail(DCU_EINVAL, "dcu_paged_attention: out or the workspace overlaps another array");
   PagedAttnArgs a;
   a.q = q;
   a.out = out;

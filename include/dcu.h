@@ -355,7 +355,9 @@ int dcu_lm_confidence_noalloc(const void *h_rows, const float *final_norm, const
  * whatever they hold then; max_rows (host) bounds the packed rows.  Rows at and
  * after row_start[B] are neither read nor written.  status (dev int32 or NULL)
  * gets the DCU_ST_* bits above ORed in; whatever the device arrays hold, no
- * access leaves the arrays as sized by the host arguments. */
+ * access leaves the arrays as sized by the host arguments.  No output, workspace
+ * or status word may overlap an input or another output: the calls refuse what
+ * they can see of it, which is all but an overlap with the pages. */
 
 /* One layer's pages.  Element (page, offset, head, d) of K is at
  * k + page * page_stride + offset * slot_stride + head * head_stride + d
@@ -379,7 +381,7 @@ typedef struct {
  * table: dev int32 [B][max_pages], every entry written; held: dev int32 [B], the
  * pages each request got; next: dev int32, *first + the pages given out -- the
  * `first` of the next call on the same pool.  B <= 65536, max_pages <= 2^27.
- * `next` may not alias `first`. */
+ * `next` may not be `first`. */
 int dcu_page_table(const int32_t *lens, int32_t B, int32_t page_size, int32_t max_pages, int32_t n_pages,
                    const int32_t *pool, int32_t n_pool, const int32_t *first, int32_t *table, int32_t *held,
                    int32_t *next, int32_t *status, dcu_stream_t stream);

@@ -155,3 +155,37 @@ def test_binding_refuses_sizes_past_32_bits(L, call):
     """ctypes keeps the low 32 bits of an integer: 2^32 + 16 would become 16."""
     with pytest.raises(ValueError, match="sizes above"):
         call(torch.zeros(4, dtype=torch.int32), torch.zeros(2, 16, 4, 64))
+
+
+# arrays far apart: what follows moves one output onto another array, 4 bytes of overlap each time
+APART = {
+    "dcu_page_table": dict(TABLE, lens=1 << 20, pool=2 << 20, first=3 << 20, table=4 << 20, held=5 << 20, next=6 << 20,
+                           status=7 << 20),
+    "dcu_slot_map": dict(MAP, table=1 << 20, count=2 << 20, pos=None, first=3 << 20, row_start=4 << 20,
+                         row_pos=5 << 20, slot=6 << 20, status=7 << 20),
+    "dcu_paged_write": dict(WRITE, qkv=1 << 20, n_rows=2 << 20, row_pos=3 << 20, slot=4 << 20, rope=5 << 20,
+                            q=6 << 20, status=7 << 20, pages=dict(k=1 << 30, v=2 << 30)),
+    "dcu_paged_attention": dict(ATTN, q=1 << 20, row_start=2 << 20, kv_len=3 << 20, table=4 << 20, out=5 << 20,
+                                ws=1 << 34, status=7 << 20, pages=dict(k=1 << 30, v=2 << 30)),
+}
+
+
+@pytest.mark.parametrize("fn,move", [
+    ("dcu_page_table", dict(held=1 << 20)), ("dcu_page_table", dict(held=(1 << 20) + 4)),
+    ("dcu_page_table", dict(table=(2 << 20) - 28)), ("dcu_page_table", dict(next=(2 << 20) + 28)),
+    ("dcu_page_table", dict(table=3 << 20)), ("dcu_page_table", dict(held=(4 << 20) + 28)),
+    ("dcu_page_table", dict(next=(5 << 20) + 4)), ("dcu_page_table", dict(status=6 << 20)),
+    ("dcu_slot_map", dict(row_start=2 << 20)), ("dcu_slot_map", dict(row_pos=(1 << 20) + 28)),
+    ("dcu_slot_map", dict(slot=(3 << 20) + 4)), ("dcu_slot_map", dict(slot=(5 << 20) - 12)),
+    ("dcu_slot_map", dict(row_start=6 << 20)), ("dcu_slot_map", dict(pos=5 << 20, pos_stride=4, first=None)),
+    ("dcu_slot_map", dict(status=(5 << 20) + 12)),
+    ("dcu_paged_write", dict(q=3 << 20)), ("dcu_paged_write", dict(q=4 << 20)), ("dcu_paged_write", dict(q=2 << 20)),
+    ("dcu_paged_write", dict(q=(5 << 20) + 64 * 64 * 4 - 16)), ("dcu_paged_write", dict(status=6 << 20)),
+    ("dcu_paged_attention", dict(ws=1 << 20)), ("dcu_paged_attention", dict(ws=5 << 20)),
+    ("dcu_paged_attention", dict(out=2 << 20)), ("dcu_paged_attention", dict(out=3 << 20)),
+    ("dcu_paged_attention", dict(out=4 << 20)), ("dcu_paged_attention", dict(status=(1 << 20) + 4096 - 4)),
+    ("dcu_paged_attention", dict(kv_len=(1 << 34) + 1024))])
+def test_outputs_over_other_arrays_are_refused(L, fn, move):
+    """Threads read the inputs and write the outputs in no order: a call in place would give wrong answers."""
+    assert _call(getattr(L, fn), APART[fn], **move) == dcu.DCU_EINVAL
+    assert fn.encode() in L.dcu_last_error(None) and b"overlap" in L.dcu_last_error(None)
