@@ -156,19 +156,22 @@ __device__ __forceinline__ void pdl_enter() {
 // kernel's CTAs are scheduled while this one runs; a GEMM CTA needs 220 KB of
 // shared memory, which an SM configured for a small carveout cannot give until
 // it drains.
-inline void prefer_max_smem(const void *kern) {
+inline void prefer_max_smem(const void *kern) noexcept {
   static std::mutex mu;
   static std::vector<std::pair<const void *, int>> done;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return;
-  std::lock_guard<std::mutex> lock(mu);
-  for (const auto &d : done)
-    if (d.first == kern && d.second == dev) return;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
-      cudaSuccess)
-    done.emplace_back(kern, dev);
-  else
-    cudaGetLastError();
+  try {
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto &d : done)
+      if (d.first == kern && d.second == dev) return;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
+        cudaSuccess)
+      done.emplace_back(kern, dev);
+    else
+      cudaGetLastError();
+  } catch (...) {  // no memory for the record: the next launch asks again.  Launches start at C entry points.
+  }
 }
 
 // Launch with programmatic stream serialization: the kernel's CTAs may be
