@@ -353,7 +353,8 @@ int dcu_lm_confidence_noalloc(const void *h_rows, const float *final_norm, const
  *
  * The counts and lengths stay on the device, so a captured call replays with
  * whatever they hold then; max_rows (host) bounds the packed rows.  Rows at and
- * after row_start[B] are neither read nor written.  status (dev int32 or NULL)
+ * after row_start[B] are not written, and nothing depends on what they hold (the
+ * write may load them before it knows the row count).  status (dev int32 or NULL)
  * gets the DCU_ST_* bits above ORed in; whatever the device arrays hold, no
  * access leaves the arrays as sized by the host arguments.  No output, workspace
  * or status word may overlap an input or another output: the calls refuse what

@@ -6,7 +6,7 @@ import torch
 
 from dynamic_layer_wise_b200 import dcu
 from tests import paged_ref as R
-from tests.test_gpu_paged import DT, case_inputs, i32, make_pages, status_word
+from tests.test_gpu_paged import DT, case_inputs, check_attention, i32, make_pages, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -42,6 +42,38 @@ def test_paged_write_flags_more_rows_than_there_are(used, flag):
     dcu.dcu_paged_write(qkv, i32([0, used]), i32(range(5)), i32(range(5)), None, k, v, H, q=q, status=st)
     n = max(0, min(used, 5))
     assert st.item() == flag and torch.equal(q[:n], qkv.view(5, -1, hd)[:n, :H].to(k.dtype)) and (q[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_not_in_use_may_hold_anything(dtype):
+    """Write and attention of 5 rows in buffers of 40 whose other rows hold NaN, far slots and far positions."""
+    H, KV, hd, T, n = 8, 2, 64, 40, 5
+    k, v = make_pages(3, 6, 16, KV, hd, DT[dtype], "slot")
+    qkv = torch.full((T, (H + 2 * KV) * hd), float("nan"), device="cuda")
+    qkv[:n] = torch.randn((n, (H + 2 * KV) * hd), device="cuda")
+    pos, slot = np.full(T, -2 ** 31), np.full(T, 2 ** 31 - 1)
+    pos[1::2], slot[1::2] = 2 ** 31 - 1, 7
+    pos[:n], slot[:n] = [0, 1, 2, 30, 31], [16, 17, 18, 62, 63]
+    tab, start, lens, table = dcu.dcu_rope_table(64, hd), i32([0, 3, n]), i32([3, 32]), i32([[1, 0], [2, 3]])
+
+    def run(rows):
+        kk, vv, st = k.clone(), v.clone(), status_word()
+        q = torch.full((rows, H, hd), 7.0, dtype=DT[dtype], device="cuda")
+        dcu.dcu_paged_write(qkv[:rows], start, i32(pos[:rows]), i32(slot[:rows]), tab, kk, vv, H, q=q, status=st)
+        full = q.clone()
+        full[n:] = float("nan")
+        out = torch.full_like(q, 3.0)
+        dcu.dcu_paged_attention(full, start, lens, table, kk, vv, out=out, status=st)
+        return kk, vv, q, out, st.item()
+
+    got, want = run(T), run(n)
+    assert got[4] == want[4] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[2][:n], want[2]) and (got[2][n:] == 7.0).all() and (got[3][n:] == 3.0).all()
+    # (the number of rows that there may be chooses the kernel, so the numbers agree to the roundings of two kernels)
+    assert torch.isfinite(got[3]).all()
+    for o in (got, want):
+        check_attention(o[3], o[2], start.cpu().numpy(), lens.cpu().numpy(), table.cpu().numpy(), o[0], o[1], dtype,
+                        hd ** -0.5)
 
 
 # ------------------------------------------------------------------ attention
