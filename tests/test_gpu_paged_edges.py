@@ -104,3 +104,51 @@ def test_paged_attention_flags_row_starts_out_of_order_or_range(dtype, rows):
         for a, z in zip(s, s[1:]):
             covered[a:z] = True
         assert flag == R.BAD_ROW and (out[~covered.cuda()] == 3.0).all()
+
+
+# Sequences per thread in the search for a block's range: more than one from 129 (head dims above 128, bf16), 257 (bf16),
+# 385 (float32) and 641 (tensor cores) sequences on.
+MANY = [  # dtype, H, KV, hd, page, sequences, rows of a sequence, keys up to
+    ("bf16", 2, 1, 64, 16, 700, 2, 60), ("bf16", 2, 1, 128, 5, 1500, 2, 40), ("f32", 2, 2, 64, 16, 700, 3, 50),
+    ("f32", 1, 1, 16, 7, 1500, 4, 30), ("bf16", 4, 1, 256, 16, 300, 1, 40), ("f32", 2, 1, 256, 16, 300, 2, 40),
+    ("bf16", 2, 1, 64, 16, 700, 20, 70), ("bf16", 1, 1, 128, 64, 1500, 30, 200), ("bf16", 2, 2, 224, 8, 800, 40, 30),
+    ("bf16", 2, 1, 64, 5, 700, 30, 70),
+]
+
+
+@pytest.mark.parametrize("where", ["ragged", "sparse", "first", "last"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_paged_attention_of_many_sequences(case, where):
+    """More sequences than a block has threads: all with rows, or rows in a few, in the first or in the last ones only."""
+    dtype, H, KV, hd, page, B, rows, keys = MANY[case]
+    rng = np.random.default_rng(100 + case)
+    lens, n = rng.integers(0, keys + 1, B), np.zeros(B, int)
+    if where == "ragged":
+        n = rng.integers(0, 2 * rows + 1, B)
+    else:
+        at = {"sparse": rng.choice(B, 13, replace=False), "first": np.arange(3), "last": np.arange(B - 3, B)}[where]
+        n[at] = rng.integers(1, 700, len(at)) if rows >= 8 else rng.integers(1, 9, len(at))
+        lens[at] = rng.integers(keys // 2, 4 * keys, len(at))
+    # rows behind the last sequence: the kernel is chosen by the rows there may be
+    tail = 2 + max(0, rows * B - int(n.sum()))
+    q, start, lens, table, k, v = case_inputs(200 + case, dtype, H, KV, hd, page, "slot", [int(x) for x in lens],
+                                              [int(x) for x in n], tail=tail)
+    st = status_word()
+    out = torch.full_like(q, 3.0)
+    dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v, out=out, status=st)
+    assert st.item() == 0 and (out[int(start[-1]):] == 3.0).all()
+    check_attention(out, q, start, lens, table, k, v, dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("H,KV,prompt,tokens", [(4, 4, 400, 64), (28, 4, 10, 64), (2, 2, 40, 255), (4, 4, 900, 64),
+                                                (28, 4, 90, 64)])
+def test_paged_attention_of_a_prompt_beside_tokens(H, KV, prompt, tokens):
+    """One kernel takes all sequences of a call, the one for few rows in the first three."""
+    rng = np.random.default_rng(prompt)
+    at = tokens // 3
+    rows, lens = [1] * tokens, [int(x) for x in rng.integers(0, 300, tokens)]
+    rows.insert(at, prompt)
+    lens.insert(at, prompt)
+    q, start, lens, table, k, v = case_inputs(300 + prompt, "bf16", H, KV, 64, 16, "slot", lens, rows, tail=0)
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v)
+    check_attention(out, q, start, lens, table, k, v, "bf16", 64 ** -0.5)
