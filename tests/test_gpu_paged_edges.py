@@ -6,9 +6,33 @@ import torch
 
 from dynamic_layer_wise_b200 import dcu
 from tests import paged_ref as R
-from tests.test_gpu_paged import DT, case_inputs, check_attention, i32, make_pages, status_word
+from tests.test_gpu_paged import DT, case_inputs, check_attention, f64, i32, make_pages, status_word
 
 pytestmark = pytest.mark.gpu
+
+
+def worst_error(got, q, start, lens, table, k, v, dtype, scale, p_step):
+    """Largest error of the rows in terms of its bound, the weights' rounding given."""
+    want, A, mag = R.attention(f64(q), start, lens, table, np.nan_to_num(f64(k), nan=0, posinf=0),
+                               np.nan_to_num(f64(v), nan=0, posinf=0), scale)
+    tol = R.attention_bound(want, A, mag, DT[dtype], max(1, max(lens)), q.shape[-1], p_step)
+    n = int(start[-1])
+    return np.max(np.abs(f64(got)[:n] - want[:n]) / tol[:n])
+
+
+def round_once(q, start, lens, table, k, v, scale):
+    """The mistake that the bound of two bf16 parts has to see: weights of one bf16, in fp64 otherwise."""
+    qn, kn, vn = f64(q), np.nan_to_num(f64(k), nan=0, posinf=0), np.nan_to_num(f64(v), nan=0, posinf=0)
+    out, page, KV = np.zeros(qn.shape), kn.shape[1], kn.shape[2]
+    for b, n in enumerate(lens):
+        rows, at = slice(start[b], start[b + 1]), np.arange(n)
+        for h in range(qn.shape[1] if n else 0):
+            kv = h // (qn.shape[1] // KV)
+            x = qn[rows, h] @ kn[table[b, at // page], at % page, kv].T * scale
+            w = np.exp(x - x.max(1, keepdims=True, initial=-np.inf)) if x.size else x
+            bf = torch.tensor(w).to(torch.bfloat16).double().numpy()
+            out[rows, h] = bf @ vn[table[b, at // page], at % page, kv] / w.sum(1, keepdims=True)
+    return torch.tensor(out).to(torch.bfloat16)
 
 
 # ------------------------------------------------------------------ RoPE + K/V write
@@ -152,3 +176,26 @@ def test_paged_attention_of_a_prompt_beside_tokens(H, KV, prompt, tokens):
     q, start, lens, table, k, v = case_inputs(300 + prompt, "bf16", H, KV, 64, 16, "slot", lens, rows, tail=0)
     out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v)
     check_attention(out, q, start, lens, table, k, v, "bf16", 64 ** -0.5)
+
+
+@pytest.mark.parametrize("H,KV,hd,page,layout,lens,rows,scale", [
+    (4, 2, 128, 5, "slot", [333, 70], [33, 20], None), (4, 4, 64, 20, "head", [700, 0, 129], [65, 3, 40], None),
+    (6, 2, 48, 100, "mixed", [1000, 31], [30, 50], None), (14, 2, 256, 7, "slot", [500, 20], [9, 3], None),
+    (4, 2, 64, 16, "slot", [250, 31], [40, 22], 0.0), (4, 2, 128, 16, "head", [600, 31], [70, 22], -0.1),
+    (4, 2, 208, 16, "slot", [250, 31], [40, 22], -0.07), (4, 2, 128, 16, "skew", [600, 31], [70, 22], None)])
+def test_many_rows_off_the_tensor_memory_path_keep_two_parts_of_a_weight(H, KV, hd, page, layout, lens, rows, scale):
+    """Many rows a sequence over pages, scales or strides that the tcgen05 kernel does not take: weights as a high and a
+    low bf16 part, 2^-16 in place of 2^-8, in all groups of 8 queries of a tile."""
+    q, start, lens, table, k, v = case_inputs(400 + hd, "bf16", H, KV, hd, page, "slot" if layout == "skew" else layout,
+                                              lens, rows, tail=0)
+    if layout == "skew":  # slots whose distance is no multiple of a head's
+        skew = lambda x: torch.empty((x.shape[0], page, KV * hd + 8), dtype=x.dtype, device="cuda")[..., :KV * hd].view(  # noqa: E731
+            x.shape[0], page, KV, hd).copy_(x)
+        k, v = skew(k), skew(v)
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v, scale=scale)
+    args = (q, start, lens, table, k, v)
+    sc = hd ** -0.5 if scale is None else scale
+    err = worst_error(out, *args, "bf16", sc, 2.0 ** -16)
+    assert err <= 1.0, f"error {err:.2f} times its bound"
+    if sc != 0.0:  # (equal weights are exact in one part)
+        assert worst_error(round_once(*args, sc), *args, "bf16", sc, 2.0 ** -16) > 1.0
