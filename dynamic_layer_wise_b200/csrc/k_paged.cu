@@ -251,17 +251,18 @@ __global__ void __launch_bounds__(kWriteMax)
   load4(x + half, b);
   const int sl = slot[t], p = rope ? row_pos[t] : 0, used = n_rows ? *n_rows : max_rows;
   if (t >= used) return;
-  const long long n_slots = (long long)pg.n_pages * pg.page_size;
+  const unsigned n_slots = (unsigned)pg.n_pages * (unsigned)pg.page_size;  // below 2^31
   const bool good = !rope || (p >= 0 && p < max_pos);
   if (u == 0) {
-    if (!good || (t == 0 && used > max_rows)) flag(status, DCU_ST_BAD_ROW);
-    if (sl < -1 || sl >= n_slots) flag(status, DCU_ST_BAD_PAGE);
+    const int bits = (!good || (t == 0 && used > max_rows) ? DCU_ST_BAD_ROW : 0) |
+                     ((unsigned)sl + 1u > n_slots ? DCU_ST_BAD_PAGE : 0);  // (-1 is no slot, and no fault)
+    if (bits) flag(status, bits);
   }
   T *dst;
   if (head < H) {
     dst = q + ((size_t)t * H + head) * hd + j;
   } else {
-    if (!good || sl < 0 || sl >= n_slots) return;
+    if (!good || (unsigned)sl >= n_slots) return;
     const int page = (int)((unsigned)sl / (unsigned)pg.page_size);
     dst = static_cast<T *>(is_v ? pg.v : pg.k) + (int64_t)page * pg.page_stride +
           (int64_t)(sl - page * pg.page_size) * pg.slot_stride + (int64_t)(head - H - (is_v ? KV : 0)) * pg.head_stride + j;

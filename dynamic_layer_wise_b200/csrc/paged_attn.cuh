@@ -33,11 +33,11 @@ struct Seq {
   int row0, nq, tiles, tq, nk, nblk;  // first row, queries per kv head, tiles, queries per tile, keys, blocks per item
   __device__ __forceinline__ long long units(int KV) const { return (long long)KV * tiles * nblk; }
 };
-template <int R, int KB>
+// FLAG: sets the status bits of the sequence, once a CTA (find_range's first look at it).
+template <int R, int KB, bool FLAG = false>
 __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   Seq s;
   const int r0 = a.row_start[b], r1 = a.row_start[b + 1];
-  if ((r0 < 0 || r1 < r0 || r1 > a.max_rows) && a.status) atomicOr(a.status, DCU_ST_BAD_ROW);
   const int lo = min(max(r0, 0), a.max_rows), hi = min(max(r1, 0), a.max_rows);
   const int rows = max(hi - lo, 0);
   s.row0 = lo;
@@ -46,7 +46,10 @@ __device__ __forceinline__ Seq seq_of(const PagedAttnArgs &a, int b) {
   s.tq = s.tiles ? ((s.nq + s.tiles - 1) / s.tiles + 7) / 8 * 8 : 0;
   const long long cap = (long long)a.max_pages * a.pages.page_size;
   const int n = max(a.kv_len[b], 0);
-  if (n > cap && rows && a.status) atomicOr(a.status, DCU_ST_BAD_PAGE);
+  if (FLAG) {
+    const int bits = (r0 < 0 || r1 < r0 || r1 > a.max_rows ? DCU_ST_BAD_ROW : 0) | (n > cap && rows ? DCU_ST_BAD_PAGE : 0);
+    if (bits && a.status) atomicOr(a.status, bits);
+  }
   s.nk = (int)min((long long)n, cap);
   s.nblk = max(1, (int)(((long long)s.nk + KB - 1) / KB));  // an empty sequence still gets its zeros
   return s;
@@ -144,7 +147,7 @@ __device__ __forceinline__ void find_range(const PagedAttnArgs &a, Place *place,
   if (a.B == 1) {
     Place p;
     p.b = 0;
-    p.s = seq_of<R, KB>(a, 0);
+    p.s = seq_of<R, KB, true>(a, 0);
     const long long total = p.s.units(KV);
     const long long items = (long long)KV * p.s.tiles;
     const int ranges = (int)min((long long)gridDim.x, max(items, div_ll(total + least - 1, least)));
@@ -172,7 +175,7 @@ __device__ __forceinline__ void find_range(const PagedAttnArgs &a, Place *place,
   Place p;  // with one sequence per thread (B <= 32 W) its items are kept
   p.b = b0;
   for (int b = b0; b < b1; ++b) {
-    p.s = seq_of<R, KB>(a, b);
+    p.s = seq_of<R, KB, true>(a, b);
     mine += p.s.units(KV);
     items += (long long)KV * p.s.tiles;
   }
