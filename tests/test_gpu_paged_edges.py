@@ -1,12 +1,15 @@
 """Calls of the paged K/V cache operators at the edges of what their documentation allows: what is flagged, and
 batches of many sequences."""
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
 
-from dynamic_layer_wise_b200 import dcu
+from dynamic_layer_wise_b200 import build, dcu
 from tests import paged_ref as R
-from tests.test_gpu_paged import DT, case_inputs, check_attention, f64, i32, make_pages, status_word
+from tests.test_gpu_paged import DT, case_inputs, check_attention, f64, i32, make_pages, make_table, status_word
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +202,129 @@ def test_many_rows_off_the_tensor_memory_path_keep_two_parts_of_a_weight(H, KV, 
     assert err <= 1.0, f"error {err:.2f} times its bound"
     if sc != 0.0:  # (equal weights are exact in one part)
         assert worst_error(round_once(*args, sc), *args, "bf16", sc, 2.0 ** -16) > 1.0
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 9), ("f32", 1)])
+def test_the_largest_batch(dtype, rows):
+    """65536 sequences through all four operators."""
+    B, page = 65536, 8
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(0, 20, B)
+    n = np.minimum(rng.integers(rows, rows + 2, B), lens)
+    first = lens - n
+    need = -(-lens // page)
+    n_pages, T = int(need.sum()), int(n.sum())
+    pool = rng.permutation(n_pages).astype(np.int32)
+    st = status_word()
+    table, held, nxt = dcu.dcu_page_table(i32(lens), page, 3, n_pages, i32(pool), None, st)
+    w_table, w_held, w_next, _ = R.page_table(lens, page, 3, n_pages, pool)
+    assert np.array_equal(table.cpu().numpy(), w_table) and np.array_equal(held.cpu().numpy(), w_held)
+    assert nxt.item() == w_next
+    start, rp, slot = dcu.dcu_slot_map(table, i32(n), page, n_pages, T, None, i32(first), st)
+    w_start, w_rp, w_slot, _ = R.slot_map(w_table, n, page, n_pages, T, None, first)
+    assert np.array_equal(start.cpu().numpy(), w_start) and np.array_equal(rp.cpu().numpy(), w_rp)
+    assert np.array_equal(slot.cpu().numpy(), w_slot)
+    k, v = make_pages(5, n_pages, page, 1, 16, DT[dtype], "slot")
+    qkv = torch.randn((T, 3 * 16), device="cuda")
+    q = dcu.dcu_paged_write(qkv, start, rp, slot, None, k, v, 1, status=st)
+    x = qkv.to(DT[dtype])
+    at = slot.long()
+    assert torch.equal(q[:, 0], x[:, :16]) and torch.equal(k.view(-1, 16)[at], x[:, 16:32])
+    assert torch.equal(v.view(-1, 16)[at], x[:, 32:])
+    # buffers as long as the rows that there may be: nine a sequence are many for the choice of the kernel
+    room = torch.zeros((max(T, rows * B) + 7, 1, 16), dtype=DT[dtype], device="cuda")
+    room[:T] = q
+    out = dcu.dcu_paged_attention(room, start, i32(lens), table, k, v, status=st)
+    assert st.item() == 0
+    check_attention(out, room, w_start, lens, w_table, k, v, dtype, 0.25)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 200])
+@pytest.mark.parametrize("B", [1, 3, 700])
+def test_paged_attention_without_any_rows(dtype, T, B):
+    k, v = make_pages(1, 4, 16, 2, 64, DT[dtype], "slot")
+    q, st = torch.randn((T, 4, 64), device="cuda").to(k.dtype), status_word()
+    for at in (0, T):
+        out = torch.full_like(q, 3.0)
+        dcu.dcu_paged_attention(q, i32([at] * (B + 1)), i32([40] * B), i32([[0, 1, 2]] * B), k, v, out=out, status=st)
+        assert st.item() == 0 and (out == 3.0).all()
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 50), ("f32", 3)])
+def test_paged_attention_of_rows_that_begin_later(dtype, rows):
+    """Rows before row_start[0] belong to no sequence."""
+    q, start, lens, table, k, v = case_inputs(17, dtype, 4, 2, 64, 16, "slot", [50, 60], [rows, rows], tail=9)
+    call = lambda x, s: dcu.dcu_paged_attention(x, i32(s), i32(lens), i32(table), k, v,  # noqa: E731
+                                                out=torch.full_like(x, 3.0))
+    ref = call(q, start)
+    out = call(torch.roll(q, 5, 0), start + 5)
+    assert torch.equal(out[5:5 + 2 * rows], ref[:2 * rows])
+    assert (out[:5] == 3.0).all() and (out[5 + 2 * rows:] == 3.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,KV,hd,page,lens,rows", [
+    (5000, 1, 16, 16, [90], [2]), (4097, 1, 32, 5, [40, 0, 7], [1, 3, 2]), (1800, 900, 16, 16, [70, 20], [1, 1]),
+    (700, 700, 32, 8, [33], [30]), (4, 2, 64, 4096, [5000, 4096, 4097], [3, 1, 20]), (4, 2, 64, 30000, [29999], [40])])
+def test_paged_attention_of_many_heads_and_long_pages(dtype, H, KV, hd, page, lens, rows):
+    q, start, lens, table, k, v = case_inputs(500 + hd, dtype, H, KV, hd, page, "slot", lens, rows)
+    st, out = status_word(), torch.full_like(q, 3.0)
+    dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v, out=out, status=st)
+    assert st.item() == 0 and (out[int(start[-1]):] == 3.0).all()
+    check_attention(out, q, start, lens, table, k, v, dtype, hd ** -0.5)
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 50), ("f32", 9)])
+def test_paged_attention_of_shared_pages(dtype, rows):
+    """Two sequences with one prefix, pages twice in a row of the table, and V in the pages of K."""
+    q, start, lens, table, k, v = case_inputs(18, dtype, 4, 2, 64, 16, "slot", [100, 130], [rows, rows])
+    k, v = k.nan_to_num(0, 0), v.nan_to_num(0, 0)
+    table[1, :6] = table[0, :6]
+    table[1, 7] = table[1, 6]
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v)
+    check_attention(out, q, start, lens, table, k, v, dtype, 0.125)
+    out = dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, k)
+    check_attention(out, q, start, lens, table, k, k, dtype, 0.125)
+
+
+def test_slot_map_of_more_rows_than_32_bits_count():
+    """Prefix sums of the counts pass 2^32; the rows there is room for are mapped and the rest flagged."""
+    table, n_pages = make_table(np.random.default_rng(0), [40, 40, 40], 16)
+    for count in ([3, 2 ** 31 - 1, 2 ** 31 - 1], [2 ** 31 - 1] * 3, [3, 2, 2 ** 31 - 1]):
+        st = status_word()
+        start, rp, sl = dcu.dcu_slot_map(i32(table), i32(count), 16, n_pages, 12, None, i32([1, 0, 5]), st)
+        w = [0] + [min(12, int(x)) for x in np.cumsum(np.array(count, np.int64))]
+        pos = [f + j for b, f in enumerate([1, 0, 5]) for j in range(w[b + 1] - w[b])]
+        seq = [b for b in range(3) for _ in range(w[b + 1] - w[b])]
+        assert start.cpu().tolist() == w and rp.cpu().tolist() == pos and st.item() == R.BAD_ROW
+        assert sl.cpu().tolist() == [int(table[b, p // 16]) * 16 + p % 16 for b, p in zip(seq, pos)]
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_captured_call_may_be_the_first(rows):
+    """Nothing has to run before a capture: kernels, limits and tensor maps are set up within it."""
+    code = f"""
+import torch
+from dynamic_layer_wise_b200 import dcu
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+k = torch.randn(8, 16, 2, 64, device="cuda").to(torch.bfloat16)
+v = torch.randn_like(k)
+qkv = torch.randn({rows}, 8 * 64, device="cuda")
+lens, count, first = i32([100]), i32([{rows}]), i32([100 - {rows}])
+torch.cuda.synchronize()
+def step():
+    table, _, _ = dcu.dcu_page_table(lens, 16, 7, 8)
+    start, pos, slot = dcu.dcu_slot_map(table, count, 16, 8, {rows}, None, first)
+    rope = dcu.dcu_rope_table(100, 64)
+    q = dcu.dcu_paged_write(qkv, start, pos, slot, rope, k, v, 4)
+    return dcu.dcu_paged_attention(q, start, lens, table, k, v)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, step()) and out.abs().max() > 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=build.ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
