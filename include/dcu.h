@@ -436,7 +436,15 @@ int dcu_paged_write(const float *qkv, int32_t max_rows, const int32_t *n_rows, c
  * whose row start lies above the next one has no rows (DCU_ST_BAD_ROW for both);
  * where row starts decrease, rows may belong to two sequences, and what out holds
  * in the rows that any sequence covers is unspecified.
- * The keys are split over the SMs and joined in a fixed order: equal inputs
+ * A score of +inf or NaN makes its row NaN, one of -inf has no weight (a row of
+ * nothing else gives zeros); a V element that is not finite makes its dim of the rows
+ * inf or NaN.  Scores, the softmax and its sums are fp32.  The weights that multiply
+ * V are fp32 for DCU_F32; for DCU_BF16 they are rounded to 16 bits (a high and a low
+ * bf16) or, above 8 queries (rows x query heads of a kv head) a sequence on average
+ * -- max_rows over B -- with scale > 0, a page_size that is a multiple of 8 and
+ * strides each a multiple of the next smaller one and not inside it, to one bf16.  So a
+ * row's last bits depend on max_rows and B.
+ * The keys are split over the SMs and joined in a fixed order: equal calls
  * give equal bits.  workspace: dev, 16-byte aligned, at least
  * dcu_paged_attention_workspace bytes, any content; calls that may overlap (on
  * other streams, or in graphs replayed together) need one each.  B <= 65536,

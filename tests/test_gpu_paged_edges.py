@@ -275,6 +275,43 @@ def test_paged_attention_of_many_heads_and_long_pages(dtype, H, KV, hd, page, le
     check_attention(out, q, start, lens, table, k, v, dtype, hd ** -0.5)
 
 
+@pytest.mark.parametrize("dtype,rows,page", [("bf16", 2, 16), ("bf16", 2, 5), ("bf16", 50, 16), ("bf16", 50, 5), ("f32", 9, 16)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_cached_value_that_is_not_finite_stays_with_its_sequence_head_and_dim(dtype, rows, page, bad):
+    q, start, lens, table, k, v = case_inputs(19, dtype, 4, 2, 64, page, "slot", [700, 200], [rows, rows], tail=0)
+    call = lambda k, v: dcu.dcu_paged_attention(q, i32(start), i32(lens), i32(table), k, v)  # noqa: E731
+    ref = call(k, v)
+    at = 333  # a key of the first sequence, kv head 1 (query heads 2 and 3)
+    kb, vb = k.clone(), v.clone()
+    vb[table[0, at // page], at % page, 1, 7] = bad
+    out, hit = call(k, vb), torch.zeros_like(ref, dtype=torch.bool)
+    hit[:rows, 2:, 7] = True
+    assert torch.equal(out[~hit], ref[~hit]) and not out[hit].isfinite().any()
+    # a key: scores of +inf or NaN make their rows NaN, a score of -inf has no weight
+    kb[table[0, at // page], at % page, 1, 7] = bad
+    out, hit = call(kb, v), torch.zeros_like(ref, dtype=torch.bool)
+    lost = (q[:rows, 2:, 7].float() * bad) != float("-inf")
+    hit[:rows, 2:] = lost[..., None]
+    assert out[hit].isnan().all() and out[~hit].isfinite().all()
+    rest = torch.ones_like(ref, dtype=torch.bool)
+    rest[:rows, 2:] = False
+    assert torch.equal(out[rest], ref[rest])
+    there = np.delete(np.arange(700), at)  # the other keys, for the rows that gave this one no weight
+    kn, vn = (f64(x)[table[0, there // page], there % page, 1] for x in (k, v))
+    for r, h in torch.nonzero(~lost).tolist():
+        x = kn @ f64(q[r, 2 + h]) / 8
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        # weights off by 2^-8 at most, the result by half a step, and 64 + 700 fp32 sums
+        assert np.all(np.abs(f64(out[r, 2 + h]) - w @ vn) <= (2.0 ** -8 + 1e-4) * (w @ np.abs(vn)) + 2.0 ** -8 * np.abs(w @ vn))
+    # no key with a weight: zeros
+    qp = q.clone()
+    qp[:rows, 2:, 7] = 1.0
+    kb[torch.tensor(table[0, np.arange(700) // page]).long(), torch.arange(700) % page, 1, 7] = float("-inf")
+    out = dcu.dcu_paged_attention(qp, i32(start), i32(lens), i32(table), kb, v)
+    assert (out[:rows, 2:] == 0).all() and torch.equal(out[rest], ref[rest])
+
+
 @pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 50), ("f32", 9)])
 def test_paged_attention_of_shared_pages(dtype, rows):
     """Two sequences with one prefix, pages twice in a row of the table, and V in the pages of K."""
