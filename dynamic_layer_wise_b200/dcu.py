@@ -437,10 +437,12 @@ def _dims(t, name: str, n: int):
     return t.shape
 
 
-def _sizes(bits: int):
-    """Refuses sizes, OR-ed together, of which one is above 2^31 - 1: ctypes would pass its low 32 bits."""
-    if bits > 0x7fffffff:
-        raise ValueError("sizes above 2^31 - 1 are not supported")
+# ctypes passes the low 32 bits of an integer.  Sizes are OR-ed together and compared with this once a call.
+_MAX = 0x7fffffff
+
+
+def _too_large():
+    raise ValueError("sizes above 2^31 - 1 are not supported")
 
 
 def _pages(k_pages, v_pages, device) -> dcu_pages:
@@ -456,7 +458,8 @@ def _pages(k_pages, v_pages, device) -> dcu_pages:
     if (sd != 1 and d != 1) or 0 in shape:
         raise ValueError(f"k_pages: expected [n_pages][page_size][n_kv_heads][head_dim] with a contiguous last "
                          f"dimension, got {tuple(shape)} with strides {strides}")
-    _sizes(n | p | h | d)
+    if (n | p | h | d) > _MAX:
+        _too_large()
     return dcu_pages(k_pages.data_ptr(), v_pages.data_ptr(), sn if n > 1 else 0, sp if p > 1 else 0,
                      sh if h > 1 else 0, n, p, h, d, _DTYPE_CODE[k_pages.dtype])
 
@@ -470,7 +473,8 @@ def dcu_page_table(lens, page_size: int, max_pages: int, n_pages: int, pool=None
     n_pool = n_pages if pool is None else _dims(pool, "pool", 1)[0]
     if max_pages <= 0:
         raise ValueError("max_pages must be positive")
-    _sizes(B | page_size | max_pages | n_pages | n_pool)
+    if (B | page_size | max_pages | n_pages | n_pool) > _MAX:
+        _too_large()
     return _run(dev, stream, _page_table, (
         lens, _arg(lens, "lens", _I32, (B,), dev), B, page_size, max_pages, n_pages,
         _opt(pool, "pool", _I32, (n_pool,), dev), n_pool, _opt(first, "first", _I32, (1,), dev),
@@ -498,7 +502,8 @@ def dcu_slot_map(table, count, page_size: int, n_pages: int, max_rows: int, pos=
         raise ValueError("pos: expected at least one column")
     if max_rows < 0:
         raise ValueError("max_rows must not be negative")
-    _sizes(B | max_pages | page_size | n_pages | N | max_rows)
+    if (B | max_pages | page_size | n_pages | N | max_rows) > _MAX:
+        _too_large()
     return _run(dev, stream, _slot_map, (
         count, _arg(table, "table", _I32, (B, max_pages), dev), B, max_pages, page_size, n_pages,
         _arg(count, "count", _I32, (B,), dev), _opt(pos, "pos", _I32, (B, N), dev), N,
@@ -518,7 +523,8 @@ def dcu_rope_table(max_pos: int, head_dim: int, theta: float = 10000.0, device="
     """(cos, sin) of pos * theta^(-2j / head_dim): float32 [max_pos][head_dim / 2][2]."""
     if max_pos <= 0 or head_dim <= 0 or head_dim % 2:
         raise ValueError("max_pos and head_dim must be positive, head_dim even")
-    _sizes(max_pos | head_dim)
+    if (max_pos | head_dim) > _MAX:
+        _too_large()
     dev = torch.device(device)
     if dev.type != "cuda":
         raise ValueError("expected a CUDA device")
@@ -551,7 +557,8 @@ def dcu_paged_write(qkv, row_start, row_pos, slot, rope, k_pages, v_pages, n_hea
     max_pos = 0 if rope is None else _dims(rope, "rope", 3)[0]
     if rope is not None and not max_pos:  # its address is NULL, which the library takes for no rotation
         raise ValueError("rope: expected at least one position")
-    _sizes(T | max_pos | n_heads)
+    if (T | max_pos | n_heads) > _MAX:
+        _too_large()
     if q is not None:
         _arg(q, "q", k_pages.dtype, (T, n_heads, hd), dev)
     return _run(dev, stream, _paged_write, (
@@ -581,7 +588,8 @@ def dcu_paged_attention(q, row_start, kv_len, table, k_pages, v_pages, scale: fl
     dev = q.device
     pages = _pages(k_pages, v_pages, dev)
     B, max_pages = _dims(table, "table", 2)
-    _sizes(T | H | B | max_pages)
+    if (T | H | B | max_pages) > _MAX:
+        _too_large()
     if out is not None:
         _arg(out, "out", q.dtype, (T, H, hd), dev)
     if workspace is not None:
