@@ -42,7 +42,8 @@ __device__ __forceinline__ long long scan64(long long v, long long *red, long lo
 // instead of waiting for another CTA.
 // Measured: 4 requests 2.6 us (a launch), 2000 ragged ones of up to 1024 pages
 // (8 MB of table, 3.7 MB of pool) 7.4 us, 1.6 TB/s: short of memory's rate (1.8
-// us) by the chain launch - lengths - sums - pool entry - store.
+// us) by the chain launch - lengths - sums - pool entry - store, and by the rounds
+// of a CTA's rows (four here), each of which waits for its pool entries.
 __device__ __forceinline__ long long pages_needed(int len, int page_size, int max_pages) {
   if (len <= 0) return 0;
   const unsigned n = ((unsigned)len + (unsigned)page_size - 1u) / (unsigned)page_size;
@@ -228,8 +229,8 @@ __device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
 // rows 2.25 in place of 2.13 us, 512 rows of which 51 are used 1.72 in place of 2.07,
 // thousands of rows the same either way).  A row is
 // streamed once and written once, so memory bounds it: 6148 rows of 28 + 2 x 4
-// heads of 128 take 28.7 us, 6.0 TB/s (a plain copy: 6.46); 65 rows of 96 heads
-// 2.3 us, a launch.  q, K and V are rounded once, from the fp32 rotation.
+// heads of 128 take 29.0 us, 6.0 TB/s (a plain copy: 6.46); 65 rows of 96 heads
+// 2.1 to 2.6 us, a launch.  q, K and V are rounded once, from the fp32 rotation.
 constexpr int kWriteMax = 512;  // most threads of a CTA
 
 template <class T>

@@ -34,13 +34,15 @@
 // blocks run on the CUDA cores in fp32.
 //
 // What bounds it: reading the pages.  One row a sequence, 28/4 heads of 128:
-// 64 ragged sequences (1.06 GB) 189 us, 5.6 TB/s; one of 131072 keys (268 MB)
-// 52.6 us, 5.1 TB/s.  The rings hold 192 KB an SM, 28 MB on the GPU; loaded key by
+// 64 ragged sequences (1.06 GB) 186 us, 5.7 TB/s; one of 131072 keys (268 MB)
+// 52.2 us, 5.1 TB/s.  The rings hold 192 KB an SM, 28 MB on the GPU; loaded key by
 // key with cp.async, 64 x 8192 keys took 289 us instead of 197.  Short calls are a
 // chain of latencies (lengths, table, keys, blocks, joins): 33 float32 rows over
-// 256 keys of 4 heads 9.7 us.  float32 blocks of head dim 256 leave room for 4
-// warps only: 2.0 TB/s over 32 x 8192 keys.  float32 head dims up to 128 take 4.9
-// TB/s with 7 queries in the tile, 3.6 with one, whose tile is as much work.
+// 256 keys of 4 heads 9.7 us.  float32, one row over 32 x 8192 keys: 5.5 TB/s with
+// 16/16 heads of 128, 5.1 with 28/4, 4.1 with head dim 256 (room for 4 warps only); a
+// group of 16 heads has two tiles, which each read the keys (2.0 TB/s of them).  Over
+// one sequence of 8192 keys 16/16 heads take 3.7 TB/s, and many rows compute 11 to 21
+// TFLOP/s in tiles of 8 queries.
 #include "paged_attn.cuh"
 #include "tc_ptx.cuh"
 
@@ -930,7 +932,8 @@ cudaError_t launch_paged_attention(const PagedAttnArgs &a, void *ws, cudaStream_
   // the tcgen05 kernel where it applies.  Measured, this kernel / that one, us a call: 1 x 1024 keys, 32 heads x 128:
   // 1 query 10.9 / 13.3, 9 queries 12.7 / 13.5; 1 x 8192 keys: 8 queries 30.0 / 34.2, 12 queries 44.4 / 34.5; 64 x
   // 2000 keys, 28/4 heads: 7 queries 53 / 58, 14 queries 91 / 59; 128 x 100 keys, 8 heads x 64: 8 queries 30.5 / 37.9,
-  // 12 queries 50.5 / 38.4.
+  // 12 queries 50.5 / 38.4.  These are of equal rows a sequence.  The rule sees a mean only, and one kernel takes all: 64
+  // tokens over 200 to 2000 keys and a prompt of 400 rows, 32 heads x 128, take 400 us together, 261 and 21 apart.
   if ((long long)a.max_rows * (a.n_heads / a.pages.n_kv_heads) <= 8ll * a.B)
     return hd <= 64 ? launch<64, false, 1>(a, ws, s)
                     : hd <= 128 ? launch<128, false, 1>(a, ws, s) : launch<256, false, 1>(a, ws, s);

@@ -60,6 +60,8 @@ struct Place {
   int b, kvh, tile, blk;
   Seq s;
 };
+// The next sequence with rows.  Those without are passed one by one, about 80 ns each: one row of 8 heads x 64 over 500
+// keys takes 7.7 us alone, 44 us with 500 sequences without rows behind it.
 template <int R, int KB>
 __device__ __forceinline__ void next_seq(const PagedAttnArgs &a, Place &p) {
   while (++p.b < a.B) {
