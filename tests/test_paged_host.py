@@ -189,3 +189,15 @@ def test_outputs_over_other_arrays_are_refused(L, fn, move):
     """Threads read the inputs and write the outputs in no order: a call in place would give wrong answers."""
     assert _call(getattr(L, fn), APART[fn], **move) == dcu.DCU_EINVAL
     assert fn.encode() in L.dcu_last_error(None) and b"overlap" in L.dcu_last_error(None)
+
+
+REFUSALS = [("dcu_page_table", test_page_table_refusals), ("dcu_slot_map", test_slot_map_refusals),
+            ("dcu_paged_write", test_paged_write_refusals), ("dcu_paged_attention", test_paged_attention_refusals)]
+
+
+@pytest.mark.parametrize("fn,bad", [(fn, bad) for fn, t in REFUSALS for bad in t.pytestmark[0].args[1]
+                                    if bad not in (dict(first=P + 64), dict(out=P))])
+def test_refusals_do_not_rest_on_an_overlap(L, fn, bad):
+    """The arguments refused above, on arrays that lie apart (the two left out are overlaps themselves)."""
+    assert _call(getattr(L, fn), APART[fn], **bad) == dcu.DCU_EINVAL
+    assert b"overlap" not in L.dcu_last_error(None)
